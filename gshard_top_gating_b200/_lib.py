@@ -21,6 +21,7 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_BWD_SKIP_EMPTY_EXPERTS = 1
 MOE_BUF_X, MOE_BUF_H, MOE_BUF_Y = 0, 1, 2
 MOE_ROUTE_REROUTE = 1
+MOE_GLU_SILU, MOE_GLU_GELU, MOE_GLU_RELU = range(3)
 MOE_NUM_STAGES = 6
 STAGES = ("router", "scan", "dispatch", "ffn1", "ffn2", "combine")
 MOE_NUM_BWD_STAGES = 8
@@ -83,6 +84,14 @@ def _load() -> ctypes.CDLL:
         "moe_ep_aux_loss": [P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)],
         "moe_ep_get_routing": [P, P, P, P, P, P, P],
         "moe_ep_check": [P, P],
+    })
+    sig.update({
+        "moe_glu_create": [ctypes.POINTER(P), I32, I64, I64, I64, ctypes.c_int, ctypes.c_int, P, P],
+        "moe_glu_destroy": [P],
+        "moe_glu_forward": [P, I64, P, P, P, P],
+        "moe_glu_enable_backward": [P],
+        "moe_glu_backward": [P, I64, P, P, P, P, P, P, ctypes.c_uint32, P],
+        "moe_glu_check": [P, P],
     })
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -379,3 +388,33 @@ def moe_ep_get_routing(h, eidx=None, gate=None, slot=None, spos=None, logits=Non
 
 def moe_ep_check(h, stream=None) -> None:
     _check("moe_ep_check", lib.moe_ep_check(h, _stream(stream)))
+
+
+# ---- gated experts
+
+def moe_glu_create(E, C_max, M, H, act, fn, W13, W2) -> int:
+    h = ctypes.c_void_p()
+    dt = MOE_BF16 if act in ("bf16", torch.bfloat16, MOE_BF16) else MOE_F32
+    _check("moe_glu_create", lib.moe_glu_create(ctypes.byref(h), E, C_max, M, H, dt, int(fn), _ptr(W13), _ptr(W2)))
+    return h.value
+
+
+def moe_glu_destroy(h) -> None:
+    _check("moe_glu_destroy", lib.moe_glu_destroy(h))
+
+
+def moe_glu_forward(h, C, x, nrows, y, stream=None) -> None:
+    _check("moe_glu_forward", lib.moe_glu_forward(h, C, _ptr(x), _ptr(nrows), _ptr(y), _stream(stream)))
+
+
+def moe_glu_enable_backward(h) -> None:
+    _check("moe_glu_enable_backward", lib.moe_glu_enable_backward(h))
+
+
+def moe_glu_backward(h, C, x, nrows, dy, dx, dW13, dW2, flags=0, stream=None) -> None:
+    _check("moe_glu_backward", lib.moe_glu_backward(h, C, _ptr(x), _ptr(nrows), _ptr(dy), _ptr(dx), _ptr(dW13),
+                                                    _ptr(dW2), int(flags), _stream(stream)))
+
+
+def moe_glu_check(h, stream=None) -> None:
+    _check("moe_glu_check", lib.moe_glu_check(h, _stream(stream)))

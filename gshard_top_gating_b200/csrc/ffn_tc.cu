@@ -20,10 +20,9 @@
 // epilogue of one tile overlaps the main loop of the next.  Tiles are ordered
 // (expert, n-tile, m-tile) with m fastest, so the CTAs working at the same time
 // share one weight column strip through L2.  All waits are bounded.
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "tc_tile.cuh"
 
 namespace moe {
 
@@ -52,13 +51,6 @@ struct Cfg {
   static_assert(TMEM_COLS <= 512, "TMEM columns");
 };
 
-// Shared-memory matrix descriptor, 128-byte swizzle (tcgen05 format: version 1 at bit 46,
-// layout type 2 = SWIZZLE_128B at bits 61-63).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, M=128, N=BN; a_mn / b_mn
 // select the MN-major (transposed) operand layout (bits 15 / 16), else K-major.
 template <int BN>
@@ -66,23 +58,6 @@ __device__ __forceinline__ uint32_t idesc_bf16(bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 }
-
-// Walks this CTA's tiles in the global order (expert, n-tile, m-tile).
-struct TileIter {
-  const int* tile_pre;   // smem [E+1]: first tile of each expert
-  const int* mtiles;     // smem [E]
-  int E, NT, e;
-  __device__ bool decode(int tile, int& ex, int& mt, int& nt) {
-    if (tile >= tile_pre[E]) return false;
-    while (tile >= tile_pre[e + 1]) ++e;
-    const int local = tile - tile_pre[e];
-    const int m_e = mtiles[e];
-    nt = local / m_e;
-    mt = local - nt * m_e;
-    ex = e;
-    return true;
-  }
-};
 
 // Epilogue modes: plain store, ReLU, or the backward's ReLU mask (keep the
 // accumulator where the first layer's saved output h is > 0, else 0).
@@ -123,13 +98,6 @@ __device__ __forceinline__ uint32_t positive_bits(const uint4 (&v)[4]) {
 // writes whole 128-byte rows, instead of each thread storing 16 bytes to 32
 // different rows per instruction.  `mrow` (kEpiMask) points at this lane's row of h
 // at the tile's first column; `zero` stores zeros without reading TMEM.
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 template <int BN, int EPI>
 __device__ __forceinline__ void store_rows(const CUtensorMap* tmD, uint32_t tmem_rows,
                                            uint32_t stage, int row0, int col0, int lane,
@@ -1143,37 +1111,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
-// 2-D row-major tensor of `outer` rows x `inner` elements (row pitch `pitch` bytes,
-// 0 = dense), 128-byte swizzle.
-bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in,
-               uint32_t box_out, bool f32 = false, uint64_t pitch = 0) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const uint64_t es = f32 ? 4 : 2;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch ? pitch : inner * es};
-  cuuint32_t box[2] = {box_in, box_out};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 template <int EPI, bool BKM>

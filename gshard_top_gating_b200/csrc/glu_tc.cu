@@ -1,0 +1,823 @@
+// glu_tc.cu -- gated experts on 5th-generation tensor cores (tcgen05), bf16 in, fp32 accumulate.
+//
+// For each expert e, with n = the rows it holds, W13 = [Wg | Wu] [M, 2H] and W2 [H, M]:
+//
+//   up     g = x Wg, u = x Wu, h = f(g) * u      one kernel: both products, f and the product
+//   down   y = h W2
+//   dh     dh = dy W2^T, dg = dh * u * f'(g), du = dh * f(g)    one kernel
+//   dx     dx = [dg | du] W13^T
+//   dW     dW13 = x^T [dg | du], dW2 = h^T dy                   reduction over the n rows
+//
+// Every product runs on CTA pairs (cta_group::2): a 256 x 256 tile of the accumulator, CTA r
+// of the pair holding rows [128r, 128r + 128) of A and columns [128r, 128r + 128) of B, and,
+// in its TMEM, its 128 rows of all 256 columns.  In `up` the pair's first CTA loads 128
+// columns of Wg and the second the same 128 columns of Wu: g and u of one element then lie
+// in one TMEM lane, 128 columns apart, and the epilogue forms h in registers.
+//
+// The caller's rows (x, y, dy, dx) are [E, C, width] with any C; rows at or past n are
+// neither read as data nor written.  Whole 32-row groups leave by TMA; the last group of an
+// expert is stored row by row.  The internal rows (h, [g|u], [dg|du]) are [E, Cp, width]
+// with Cp a multiple of 256, and the rows of an expert's last tile past n are stored as
+// zeros in training, since the weight gradients reduce over whole blocks of 64 rows.
+//
+// Roles per CTA (192 threads): warp 0 loads (TMA), warp 1 issues MMAs (the pair's first CTA)
+// and owns TMEM, warps 2..5 drain the accumulator, double buffered, while the next tile's
+// products run.  Every wait is bounded.
+#include "common.cuh"
+#include "glu.cuh"
+#include "internal.h"
+#include "tc_tile.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BK = 64;                 // depth of a stage
+constexpr int PM = 256, PN = 256;      // pair tile
+constexpr int kThreads = 192;
+constexpr uint32_t A_BYTES = 128 * BK * 2;            // 16 KB: 128 rows of A
+constexpr uint32_t B_BYTES = 128 * BK * 2;            // 16 KB: 128 columns of B
+constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;   // per CTA
+constexpr uint32_t TMEM_COLS = 2 * PN;                // double-buffered accumulator
+constexpr uint32_t TILE_BYTES = 4096;                 // a 32-row x 64-column bf16 store tile
+constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;        // shared::cluster address -> the pair's first CTA
+
+enum { kUp = 0, kUpSave = 1, kDown = 2, kDh = 3, kDx = 4, kDw = 5 };
+
+// Store tiles per epilogue warp: h; h, g and u; one; two buffers of (g, u), which dg and du
+// leave through; one; one.
+constexpr int store_tiles(int mode) { return mode == kUpSave ? 3 : mode == kDh ? 4 : 1; }
+constexpr int stages(int mode) { return mode == kUpSave ? 5 : mode == kDh ? 4 : 6; }
+constexpr uint32_t kBars = 512;
+constexpr size_t smem_bytes(int mode) {
+  // alignment slack, stages, store tiles, barriers, misc, tile tables
+  return 1024 + (size_t)stages(mode) * STAGE_BYTES + 4 * store_tiles(mode) * TILE_BYTES + kBars + 16 +
+         4 * (3 * kMaxExperts + 1);
+}
+// A CTA owns its SM (see the expert GEMMs of ffn_tc.cu): no other TMEM user fits beside it.
+static_assert(smem_bytes(kUp) <= 227 * 1024 && smem_bytes(kUpSave) <= 227 * 1024 &&
+              smem_bytes(kDh) <= 227 * 1024, "shared memory per CTA");
+static_assert(smem_bytes(kUp) + 81 * 1024 > 228 * 1024 && smem_bytes(kUpSave) + 81 * 1024 > 228 * 1024 &&
+              smem_bytes(kDh) + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
+
+struct PairArgs {
+  const int32_t* n;      // [E] rows per expert, clamped to [0, C]
+  int E, C;
+  int64_t Ca, Cb, Cd;    // rows per expert of A, of B (kDw) and of the output
+  int K, N;              // depth (kDw: unused) and output columns (kUp: H; kDw: Q)
+  int P;                 // kDw: output rows per expert
+  int tailA, tailB;      // kDw: the last, partial 64-row block comes from the tail maps
+  int store_zero;        // kDw: experts without rows get zeros (else keep what they hold)
+  __nv_bfloat16* D;      // output, for the row-by-row stores (kDown, kDx)
+  unsigned* err;
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ int rows_of(const PairArgs& a, int e) { return min(max(a.n[e], 0), a.C); }
+
+// idesc: kind::f16, D fp32, A and B bf16, M = 256, N = 256; a_mn / b_mn: operand's rows or
+// columns contiguous instead of its depth.
+__device__ __forceinline__ uint32_t idesc_pair(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+}
+
+// 32 packed bf16 (16 words) of this lane's row into a 128-byte-swizzled store tile, columns
+// [32 half, 32 half + 32).
+__device__ __forceinline__ void put_half(uint32_t tile, int lane, int half, const uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    st_shared_v4(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
+                 pk[4 * j + 3]);
+}
+__device__ __forceinline__ void get_half(uint32_t tile, int lane, int half, uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = ld_shared_v4(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4));
+    pk[4 * j] = v.x;
+    pk[4 * j + 1] = v.y;
+    pk[4 * j + 2] = v.z;
+    pk[4 * j + 3] = v.w;
+  }
+}
+
+// Plain output of one warp: 32 rows x 256 columns from column col0 (N columns, a multiple
+// of 64), nvalid of the rows kept (and row stores where that is fewer than 32).
+__device__ __forceinline__ void store_plain(const CUtensorMap* tmD, uint32_t tmem, uint32_t tile, int64_t row0, int col0,
+                                            int N, int nvalid, bool zero, __nv_bfloat16* D, int lane) {
+#pragma unroll 1
+  for (int b = 0; b < PN / 64; ++b) {
+    const int col = col0 + b * 64;
+    if (col >= N) return;
+    if (nvalid == 32) {
+      if (lane == 0) bulk_wait_read0();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t r[32], pk[16];
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = 0u;
+      } else {
+        tmem_ld_32x32b_x32(tmem + b * 64 + half * 32, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      }
+      if (nvalid == 32) {
+        put_half(tile, lane, half, pk);
+      } else if (lane < nvalid) {
+        uint4* p = reinterpret_cast<uint4*>(D + (row0 + lane) * N + col + half * 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+      }
+    }
+    if (nvalid == 32) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d_hint(tmD, tile, col, (int)row0, l2_policy_evict_first());
+        bulk_commit();
+      }
+    }
+  }
+}
+
+// g and u of one warp's 32 rows x 128 elements -> h (tmD), and with SAVE g and u as well
+// (tmD2, [.., 2H]: g at column n, u at H + n); rows past nvalid become zeros with SAVE.
+template <int FN, bool SAVE>
+__device__ __forceinline__ void store_up(const CUtensorMap* tmD, const CUtensorMap* tmD2, uint32_t tmem, uint32_t tile,
+                                         int row0, int col0, int H, int nvalid, int lane) {
+  const bool live = !SAVE || lane < nvalid;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    const int col = col0 + b * 64;
+    if (col >= H) return;
+    if (lane == 0) bulk_wait_read0();
+    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t g[32], u[32], pk[16];
+      tmem_ld_32x32b_x32(tmem + b * 64 + half * 32, g);
+      tmem_ld_32x32b_x32(tmem + 128 + b * 64 + half * 32, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float h0 = glu_f<FN, true>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]);
+        const float h1 = glu_f<FN, true>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]);
+        pk[j] = live ? pack_bf16x2(h0, h1) : 0u;
+      }
+      put_half(tile, lane, half, pk);
+      if (SAVE) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          pk[j] = live ? pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])) : 0u;
+        put_half(tile + TILE_BYTES, lane, half, pk);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          pk[j] = live ? pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])) : 0u;
+        put_half(tile + 2 * TILE_BYTES, lane, half, pk);
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d_hint(tmD, tile, col, row0, l2_policy_evict_first());
+      if (SAVE) {
+        tma_store_2d_hint(tmD2, tile + TILE_BYTES, col, row0, l2_policy_evict_first());
+        tma_store_2d_hint(tmD2, tile + 2 * TILE_BYTES, H + col, row0, l2_policy_evict_first());
+      }
+      bulk_commit();
+    }
+  }
+}
+
+// The g and u chunk (64 columns) that starts at column col, by TMA into a pair of tiles.
+__device__ __forceinline__ void load_gu(const CUtensorMap* tmGU, uint32_t tile, uint32_t bar, int row0, int col, int H) {
+  mbar_arrive_expect_tx(bar, 2 * TILE_BYTES);
+  tma_load_2d(tile, tmGU, bar, col, row0);
+  tma_load_2d(tile + TILE_BYTES, tmGU, bar, H + col, row0);
+}
+
+// MODE kUp, kUpSave, kDown, kDh, kDx.  tmD2: kUpSave the [g|u] output, kDh the [g|u] input.
+template <int MODE, int FN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    glu_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD2,
+                    const PairArgs a) {
+  constexpr int STAGES = stages(MODE);
+  constexpr bool UP = MODE == kUp || MODE == kUpSave;
+  constexpr bool BKM = MODE == kDh || MODE == kDx;     // B's depth is contiguous
+  constexpr int COLS = UP ? 128 : PN;                  // output columns of a tile
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
+  unsigned char* gbase = smem_raw + (base - raw_base);
+  const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
+  const uint32_t bar0 = tiles0 + 4 * store_tiles(MODE) * TILE_BYTES;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
+  auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
+  const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto gu_bar = [&](int w, int i) { return bar0 + 8u * (2 * STAGES + 5 + 2 * w + i); };
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + 4 * store_tiles(MODE) * TILE_BYTES + kBars;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int* tile_pre = reinterpret_cast<int*>(misc + 16);   // [E + 1]
+  int* mtiles = tile_pre + (kMaxExperts + 1);          // [E]
+  int* nrows = mtiles + kMaxExperts;                   // [E]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int NT = (a.N + COLS - 1) / COLS;
+  const int KB = a.K / BK;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull_bar(i), 1);
+      mbar_init(tempty_bar(i), 2 * 128);       // epilogue threads of both CTAs
+    }
+    mbar_init(done_bar, 1);
+    if (MODE == kDh)
+      for (int w = 0; w < 4; ++w)
+        for (int i = 0; i < 2; ++i) mbar_init(gu_bar(w, i), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  pdl_trigger();
+  pdl_wait();                          // the producing kernel's rows and counts are complete
+  if (warp == 2) {
+    const int per = (a.E + 31) / 32;
+    const int e0 = lane * per;
+    int sum = 0;
+    for (int e = e0; e < min(a.E, e0 + per); ++e) {
+      nrows[e] = rows_of(a, e);
+      mtiles[e] = (nrows[e] + PM - 1) / PM;
+      sum += mtiles[e] * NT;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int run = inc - sum;
+    for (int e = e0; e < min(a.E, e0 + per); ++e) {
+      tile_pre[e] = run;
+      run += mtiles[e] * NT;
+    }
+    if (lane == 31) tile_pre[a.E] = inc;
+  }
+  tc_fence_before();
+  cluster_sync_all();          // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      TileIter it{tile_pre, mtiles, a.E, NT, 0};
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int e, mt, nt;
+      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+        const int rowA = (int)(e * a.Ca) + mt * PM + (int)rank * 128;
+        // first column of this CTA's half of B: the same 128 elements of Wg or of Wu, or 128
+        // of the tile's 256 columns
+        const int colB = UP ? (int)rank * a.N + nt * COLS : nt * COLS + (int)rank * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t fb = full_bar(s) & kPeerBitMask;     // the leader's full barrier
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          tma_load_2d_pair(sa, &tmA, fb, kb * BK, rowA);
+          if (BKM) {
+            tma_load_2d_pair(sa + A_BYTES, &tmB, fb, kb * BK, e * a.N + colB);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              tma_load_2d_pair(sa + A_BYTES + j * 8192u, &tmB, fb, colB + j * 64, e * a.K + kb * BK);
+          }
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (lane == 0 && leader) {
+      TileIter it{tile_pre, mtiles, a.E, NT, 0};
+      const uint32_t idesc = idesc_pair(false, !BKM);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int e, mt, nt, i = 0;
+      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs, ++i) {
+        const int acc = i & 1;
+        const uint32_t aph = (i >> 1) & 1;
+        if (*abort_flag || !mbar_wait(tempty_bar(acc), aph ^ 1u, a.err, a.limit_ns)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * PN;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t sb = sa + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = desc_sw128(sa + kk * 32u, 16u, 1024u);
+            const uint64_t bd = BKM ? desc_sw128(sb + kk * 32u, 16u, 1024u)
+                                    : desc_sw128(sb + kk * 2048u, 8192u, 1024u);
+            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kb | kk) != 0);
+          }
+          tc_commit_pair(empty_bar(s), 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
+      }
+      if (!ok) {
+        tc_commit_pair(done_bar, 0x1);
+        mbar_wait(done_bar, 0, a.err, a.limit_ns);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (warps 2..5, both CTAs)
+    const int q = warp & 3;
+    const uint32_t tile0 = tiles0 + (warp - 2) * store_tiles(MODE) * TILE_BYTES;
+    TileIter it{tile_pre, mtiles, a.E, NT, 0};
+    int e, mt, nt, i = 0;
+    uint32_t gph = 0;            // kDh: phase bits of the two (g, u) buffers
+    for (int tile = pair; it.decode(tile, e, mt, nt); tile += npairs, ++i) {
+      const int acc = i & 1;
+      const uint32_t aph = (i >> 1) & 1;
+      const int local = mt * PM + (int)rank * 128 + q * 32;     // row within the expert
+      const int64_t row0 = e * a.Cd + local;
+      const int nvalid = min(32, nrows[e] - local);
+      const int col0 = nt * COLS;
+      if (MODE == kDh && nvalid > 0 && lane == 0) {
+        bulk_wait_read0();       // the previous tile's stores have read their buffers
+        load_gu(&tmD2, tile0, gu_bar(warp - 2, 0), (int)row0, col0, a.N);
+      }
+      if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
+        *abort_flag = 1;
+        if (MODE == kDh && nvalid > 0) mbar_wait(gu_bar(warp - 2, 0), gph & 1u, a.err, a.limit_ns);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN;
+      if constexpr (UP) {
+        if (MODE == kUpSave || nvalid > 0)
+          store_up<FN, MODE == kUpSave>(&tmD, &tmD2, tm, tile0, (int)row0, col0, a.N, nvalid, lane);
+      } else if constexpr (MODE == kDh) {
+        bool ok = true;
+        const int nb = min(PN / 64, (a.N - col0 + 63) / 64);
+        if (nvalid > 0) {
+#pragma unroll 1
+          for (int b = 0; b < nb; ++b) {
+            const uint32_t buf = tile0 + (b & 1) * 2 * TILE_BYTES;
+            if (b + 1 < nb && lane == 0) {
+              // the other buffer's stores (chunk b - 1) have left; bring in chunk b + 1
+              bulk_wait_read0();
+              load_gu(&tmD2, tile0 + ((b + 1) & 1) * 2 * TILE_BYTES, gu_bar(warp - 2, (b + 1) & 1), (int)row0,
+                      col0 + (b + 1) * 64, a.N);
+            }
+            __syncwarp();
+            ok = ok && mbar_wait(gu_bar(warp - 2, b & 1), (gph >> (b & 1)) & 1u, a.err, a.limit_ns);
+            gph ^= 1u << (b & 1);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t r[32], pg[16], pu[16];
+              get_half(buf, lane, half, pg);
+              get_half(buf + TILE_BYTES, lane, half, pu);
+              tmem_ld_32x32b_x32(tm + b * 64 + half * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float d0 = __uint_as_float(r[2 * j]), d1 = __uint_as_float(r[2 * j + 1]);
+                float f0, df0, f1, df1;
+                glu_f_df<FN, true>(bf16lo(pg[j]), f0, df0);
+                glu_f_df<FN, true>(bf16hi(pg[j]), f1, df1);
+                const float u0 = bf16lo(pu[j]), u1 = bf16hi(pu[j]);
+                pg[j] = lane < nvalid ? pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1) : 0u;
+                pu[j] = lane < nvalid ? pack_bf16x2(d0 * f0, d1 * f1) : 0u;
+              }
+              put_half(buf, lane, half, pg);
+              put_half(buf + TILE_BYTES, lane, half, pu);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d_hint(&tmD, buf, col0 + b * 64, (int)row0, l2_policy_evict_first());
+              tma_store_2d_hint(&tmD, buf + TILE_BYTES, a.N + col0 + b * 64, (int)row0, l2_policy_evict_first());
+              bulk_commit();
+            }
+          }
+        } else {
+          // rows past the last one in this tile: zeros, so that the block that holds it reduces
+          // over nothing else
+#pragma unroll 1
+          for (int b = 0; b < nb; ++b) {
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+            const uint32_t z[16] = {};
+            put_half(tile0, lane, 0, z);
+            put_half(tile0, lane, 1, z);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d_hint(&tmD, tile0, col0 + b * 64, (int)row0, l2_policy_evict_first());
+              tma_store_2d_hint(&tmD, tile0, a.N + col0 + b * 64, (int)row0, l2_policy_evict_first());
+              bulk_commit();
+            }
+          }
+        }
+        if (!ok) *abort_flag = 1;
+      } else {
+        if (nvalid > 0) store_plain(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
+      }
+      tc_fence_before();
+      if (leader) mbar_arrive(tempty_bar(acc));
+      else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();          // no CTA leaves while its pair may still use its smem or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// Weight gradients D[e] = A[e, :n]^T B[e, :n] ([P, N] per expert): both operands with their
+// rows as the depth.  Rows n .. ceil64(n) - 1 of an operand hold zeros, or its last, partial
+// block is read from a tail copy ([E, 64, width], zero-filled; tailA / tailB).
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    glu_dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmAt,
+                  const __grid_constant__ CUtensorMap tmBt, const PairArgs a) {
+  constexpr int STAGES = stages(kDw);
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - raw_base);
+  const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
+  const uint32_t bar0 = tiles0 + 4 * TILE_BYTES;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
+  auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
+  const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + 4 * TILE_BYTES + kBars;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int* nrows = reinterpret_cast<int*>(misc + 16);      // [E]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int PT = (a.P + PM - 1) / PM, QT = (a.N + PN - 1) / PN;
+  const int per_e = PT * QT, total = a.E * per_e;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull_bar(i), 1);
+      mbar_init(tempty_bar(i), 2 * 128);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (warp == 2)
+    for (int e = lane; e < a.E; e += 32) nrows[e] = rows_of(a, e);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < total; tile += npairs) {
+        const int e = tile / per_e, r = tile - e * per_e;
+        const int pt = r / QT, qt = r - pt * QT;
+        const int KB = (nrows[e] + BK - 1) / BK;
+        const bool part = (nrows[e] % BK) != 0;
+        const int colA = pt * PM + (int)rank * 128, colB = qt * PN + (int)rank * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t fb = full_bar(s) & kPeerBitMask;
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          const bool last = part && kb == KB - 1;
+          const bool ta = last && a.tailA, tb = last && a.tailB;
+          const int rowA = ta ? e * BK : (int)(e * a.Ca) + kb * BK;
+          const int rowB = tb ? e * BK : (int)(e * a.Cb) + kb * BK;
+          // columns past P or N (a last tile cut short) read as zeros
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tma_load_2d_pair(sa + j * 8192u, ta ? &tmAt : &tmA, fb, colA + j * 64, rowA);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            tma_load_2d_pair(sa + A_BYTES + j * 8192u, tb ? &tmBt : &tmB, fb, colB + j * 64, rowB);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_pair(true, true);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int i = 0;
+      for (int tile = pair; ok && tile < total; tile += npairs) {
+        const int KB = (nrows[tile / per_e] + BK - 1) / BK;
+        if (KB == 0) continue;                  // zero tile: the epilogues store zeros
+        const int acc = i & 1;
+        const uint32_t aph = (i >> 1) & 1;
+        ++i;
+        if (*abort_flag || !mbar_wait(tempty_bar(acc), aph ^ 1u, a.err, a.limit_ns)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * PN;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t sb = sa + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = desc_sw128(sa + kk * 2048u, 8192u, 1024u);
+            const uint64_t bd = desc_sw128(sb + kk * 2048u, 8192u, 1024u);
+            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kb | kk) != 0);
+          }
+          tc_commit_pair(empty_bar(s), 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
+      }
+      if (!ok) {
+        tc_commit_pair(done_bar, 0x1);
+        mbar_wait(done_bar, 0, a.err, a.limit_ns);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const uint32_t tile0 = tiles0 + (warp - 2) * TILE_BYTES;
+    int i = 0;
+    for (int tile = pair; tile < total; tile += npairs) {
+      const int e = tile / per_e, r = tile - e * per_e;
+      const int pt = r / QT, qt = r - pt * QT;
+      const bool zero = nrows[e] == 0;
+      const int prow = pt * PM + (int)rank * 128 + q * 32;     // P is a multiple of 64: 32 rows or none
+      int acc = 0;
+      if (!zero) {
+        acc = i & 1;
+        const uint32_t aph = (i >> 1) & 1;
+        ++i;
+        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+      }
+      if (prow < a.P && (!zero || a.store_zero))
+        store_plain(&tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN, tile0, (int64_t)e * a.P + prow, qt * PN, a.N,
+                    32, zero, nullptr, lane);
+      if (!zero) {
+        tc_fence_before();
+        if (leader) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      }
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// The last, partial block of 64 rows of each expert of up to two row buffers, zero-filled:
+// what the weight gradients read instead of the caller's rows past the last one.
+__global__ void __launch_bounds__(256) glu_tail_kernel(const uint4* __restrict__ x0, const uint4* __restrict__ x1,
+                                                       uint4* __restrict__ t0, uint4* __restrict__ t1,
+                                                       const int32_t* __restrict__ nexp, int64_t C, int row16) {
+  pdl_wait();
+  const int e = blockIdx.x;
+  const int n = min(max(nexp[e], 0), (int)C);
+  const int first = n & ~(BK - 1), rem = n - first;
+  if (rem == 0) return;
+  const uint4* x = blockIdx.z ? x1 : x0;
+  uint4* t = (blockIdx.z ? t1 : t0) + (int64_t)e * BK * row16;
+  const uint4* src = x + ((int64_t)e * C + first) * row16;
+  const int live = rem * row16, all = BK * row16;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < all; i += gridDim.y * 256)
+    t[i] = i < live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int MODE, int FN>
+cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, const CUtensorMap& tmD2,
+                        const PairArgs& p, const GluArgs& a) {
+  auto kern = glu_pair_kernel<MODE, FN>;
+  const size_t smem = smem_bytes(MODE);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), smem, a.st, tmA, tmB, tmD, tmD2, p);
+}
+
+template <int MODE>
+cudaError_t launch_fn(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, const CUtensorMap& tmD2,
+                      const PairArgs& p, const GluArgs& a) {
+  if (a.fn == kGluSilu) return launch_pair<MODE, kGluSilu>(tmA, tmB, tmD, tmD2, p, a);
+  if (a.fn == kGluGelu) return launch_pair<MODE, kGluGelu>(tmA, tmB, tmD, tmD2, p, a);
+  return launch_pair<MODE, kGluRelu>(tmA, tmB, tmD, tmD2, p, a);
+}
+
+PairArgs pair_args(const GluArgs& a) {
+  PairArgs p{};
+  p.n = a.n;
+  p.E = a.E;
+  p.C = (int)a.C;
+  p.err = a.err;
+  p.limit_ns = a.limit_ns;
+  return p;
+}
+
+uint64_t rows(int E, int64_t per) { return (uint64_t)E * (uint64_t)per; }
+
+cudaError_t launch_dw(const GluArgs& a, const void* A, int64_t Ca, int P, const void* At, const void* B, int64_t Cb, int Q,
+                      const void* Bt, void* D) {
+  CUtensorMap tmA, tmB, tmD, tmAt, tmBt;
+  if (!encode_2d(&tmA, A, P, rows(a.E, Ca), 64, BK) || !encode_2d(&tmB, B, Q, rows(a.E, Cb), 64, BK) ||
+      !encode_2d(&tmD, D, Q, rows(a.E, P), 64, 32) ||
+      !encode_2d(&tmAt, At ? At : A, P, At ? rows(a.E, BK) : rows(a.E, Ca), 64, BK) ||
+      !encode_2d(&tmBt, Bt ? Bt : B, Q, Bt ? rows(a.E, BK) : rows(a.E, Cb), 64, BK))
+    return cudaErrorInvalidValue;
+  PairArgs p = pair_args(a);
+  p.Ca = Ca;
+  p.Cb = Cb;
+  p.P = P;
+  p.N = Q;
+  p.tailA = At != nullptr;
+  p.tailB = Bt != nullptr;
+  p.store_zero = !a.skip_empty;
+  const size_t smem = smem_bytes(kDw);
+  cudaError_t e = cudaFuncSetAttribute(glu_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(kThreads), smem, a.st, tmA, tmB, tmD, tmAt, tmBt, p);
+}
+
+}  // namespace
+
+cudaError_t glu_up_bf16(const GluArgs& a) {
+  CUtensorMap tmA, tmB, tmD, tmD2;
+  if (!encode_2d(&tmA, a.x, a.M, rows(a.E, a.C), BK, 128) ||
+      !encode_2d(&tmB, a.W13, 2 * (uint64_t)a.H, rows(a.E, a.M), 64, BK) ||
+      !encode_2d(&tmD, a.h, a.H, rows(a.E, a.Cp), 64, 32) ||
+      !encode_2d(&tmD2, a.gu ? a.gu : a.h, a.gu ? 2 * (uint64_t)a.H : a.H, rows(a.E, a.Cp), 64, 32))
+    return cudaErrorInvalidValue;
+  PairArgs p = pair_args(a);
+  p.Ca = a.C;
+  p.Cd = a.Cp;
+  p.K = a.M;
+  p.N = a.H;
+  return a.gu ? launch_fn<kUpSave>(tmA, tmB, tmD, tmD2, p, a) : launch_fn<kUp>(tmA, tmB, tmD, tmD2, p, a);
+}
+
+cudaError_t glu_down_bf16(const GluArgs& a) {
+  CUtensorMap tmA, tmB, tmD;
+  if (!encode_2d(&tmA, a.h, a.H, rows(a.E, a.Cp), BK, 128) ||
+      !encode_2d(&tmB, a.W2, a.M, rows(a.E, a.H), 64, BK) || !encode_2d(&tmD, a.y, a.M, rows(a.E, a.C), 64, 32))
+    return cudaErrorInvalidValue;
+  PairArgs p = pair_args(a);
+  p.Ca = a.Cp;
+  p.Cd = a.C;
+  p.K = a.H;
+  p.N = a.M;
+  p.D = static_cast<__nv_bfloat16*>(a.y);
+  return launch_pair<kDown, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
+}
+
+cudaError_t glu_tail_bf16(const GluArgs& a) {
+  const int row16 = a.M / 8;
+  return launch_pdl(glu_tail_kernel, dim3(a.E, (BK * row16 + 1023) / 1024, 2), dim3(256), 0, a.st,
+                    static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.dy), static_cast<uint4*>(a.tx),
+                    static_cast<uint4*>(a.tdy), a.n, a.C, row16);
+}
+
+cudaError_t glu_dh_bf16(const GluArgs& a) {
+  CUtensorMap tmA, tmB, tmD, tmG;
+  if (!encode_2d(&tmA, a.dy, a.M, rows(a.E, a.C), BK, 128) ||
+      !encode_2d(&tmB, a.W2, a.M, rows(a.E, a.H), BK, 128) ||
+      !encode_2d(&tmD, a.dgu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 64, 32) ||
+      !encode_2d(&tmG, a.gu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 64, 32))
+    return cudaErrorInvalidValue;
+  PairArgs p = pair_args(a);
+  p.Ca = a.C;
+  p.Cd = a.Cp;
+  p.K = a.M;
+  p.N = a.H;
+  return launch_fn<kDh>(tmA, tmB, tmD, tmG, p, a);
+}
+
+cudaError_t glu_dx_bf16(const GluArgs& a) {
+  CUtensorMap tmA, tmB, tmD;
+  if (!encode_2d(&tmA, a.dgu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), BK, 128) ||
+      !encode_2d(&tmB, a.W13, 2 * (uint64_t)a.H, rows(a.E, a.M), BK, 128) ||
+      !encode_2d(&tmD, a.dx, a.M, rows(a.E, a.C), 64, 32))
+    return cudaErrorInvalidValue;
+  PairArgs p = pair_args(a);
+  p.Ca = a.Cp;
+  p.Cd = a.C;
+  p.K = 2 * a.H;
+  p.N = a.M;
+  p.D = static_cast<__nv_bfloat16*>(a.dx);
+  return launch_pair<kDx, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
+}
+
+cudaError_t glu_dw2_bf16(const GluArgs& a) {
+  return launch_dw(a, a.h, a.Cp, a.H, nullptr, a.dy, a.C, a.M, a.tdy, a.dW2);
+}
+
+cudaError_t glu_dw13_bf16(const GluArgs& a) {
+  return launch_dw(a, a.x, a.C, a.M, a.tx, a.dgu, a.Cp, 2 * a.H, nullptr, a.dW13);
+}
+
+}  // namespace moe

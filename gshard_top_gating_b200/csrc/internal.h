@@ -42,6 +42,11 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// tmap.cu: 2-D row-major tensor of `outer` rows x `inner` elements (row pitch `pitch` bytes,
+// 0 = dense), bf16 or fp32, 128-byte swizzle.
+bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in,
+               uint32_t box_out, bool f32 = false, uint64_t pitch = 0);
+
 // Device tables of one forward (all owned by the handle's workspace).
 struct Routing {
   float* logits;     // [S, E]   fp32 logits as routed (bias included)
@@ -251,6 +256,45 @@ cudaError_t launch_ffn_bwd_f32(const float* xbuf, const float* hbuf, float* dybu
                                const float* W1, const float* W2, float* dW1, float* dW2,
                                const int32_t* nexp, int E, int64_t Cbuf, int M, int H,
                                bool skip_empty, cudaStream_t st);
+// Gated experts (glu_tc.cu in bf16, glu_simt.cu in fp32): h = f(x Wg) * (x Wu), y = h W2.
+enum { kGluSilu = 0, kGluGelu = 1, kGluRelu = 2 };
+struct GluArgs {
+  int E, M, H, fn;
+  int64_t C;             // rows per expert of x, y, dy, dx
+  int64_t Cp;            // rows per expert of h, gu, dgu (a multiple of 256, >= C)
+  const int32_t* n;      // [E] device: rows each expert holds, read as min(max(n, 0), C)
+  const void* x;         // [E, C, M]
+  const void* W13;       // [E, M, 2H]: Wg in columns [0, H), Wu in [H, 2H)
+  const void* W2;        // [E, H, M]
+  void* h;               // [E, Cp, H]
+  void* gu;              // [E, Cp, 2H] g and u as the backward reads them, or null (inference)
+  void* y;               // [E, C, M]
+  const void* dy;        // [E, C, M]
+  void* dgu;             // [E, Cp, 2H]
+  void* dx;              // [E, C, M]
+  void* dW13;            // [E, M, 2H]
+  void* dW2;             // [E, H, M]
+  void* tx;              // bf16: [E, 64, M] copies of the last partial 64-row block of x and of
+  void* tdy;             //   dy, or null where those rows hold zeros up to a multiple of 64
+  bool skip_empty;       // experts without rows leave dW13[e], dW2[e] as they are (else zeros)
+  unsigned* err;
+  uint64_t limit_ns;
+  int num_sms;
+  cudaStream_t st;
+};
+cudaError_t glu_up_bf16(const GluArgs& a);      // h (and gu)
+cudaError_t glu_down_bf16(const GluArgs& a);    // y
+cudaError_t glu_tail_bf16(const GluArgs& a);    // tx, tdy
+cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu
+cudaError_t glu_dx_bf16(const GluArgs& a);      // dx
+cudaError_t glu_dw2_bf16(const GluArgs& a);
+cudaError_t glu_dw13_bf16(const GluArgs& a);
+cudaError_t glu_up_f32(const GluArgs& a);
+cudaError_t glu_down_f32(const GluArgs& a);
+cudaError_t glu_dh_f32(const GluArgs& a);
+cudaError_t glu_dx_f32(const GluArgs& a);
+cudaError_t glu_dw2_f32(const GluArgs& a);
+cudaError_t glu_dw13_f32(const GluArgs& a);
 // selftest.cu
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st);
 

@@ -1,0 +1,128 @@
+"""GatedExperts: an owning wrapper around one moe_glu_* handle (marshalling only).
+
+    ex = GatedExperts(C_max, W13, W2, activation="silu")   # W13 [E, M, 2H], W2 [E, H, M]
+    y = ex(x, counts)                                       # x [E, C, M], counts int32 [E]
+    ex.enable_backward()                                    # training: forwards keep g and u
+    g = ex.backward(x, counts, dy)                          # dx, dW13, dW2
+
+Expert e holds the first counts[e] of its C rows; the rows past them are neither read as
+data nor written.  The weights are borrowed by the C library; this object keeps
+references to them so they outlive the handle.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+
+ACTIVATIONS = {"silu": L.MOE_GLU_SILU, "gelu": L.MOE_GLU_GELU, "relu": L.MOE_GLU_RELU}
+
+
+def check_tensor(name, t, shape, dtype, device) -> None:
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}, "
+                         f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+class on_stream:
+    """Context of one call: the handle's device current and `stream` (default: that device's
+    current stream) the one that new tensors are allocated on; tensors of other streams
+    that the call uses are recorded on it."""
+
+    def __init__(self, device, stream, *tensors):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the operator on {device}")
+        self.stream, self.tensors = stream, tensors
+        self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        other = self.stream != torch.cuda.current_stream(self.stream.device)
+        self.ctx.__enter__()
+        if other:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+class GatedExperts:
+    def __init__(self, C_max: int, W13: torch.Tensor, W2: torch.Tensor, activation: str = "silu"):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+        if W13.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("expert weights must be float32 or bfloat16")
+        if not W13.is_cuda or W13.dim() != 3 or W13.shape[2] % 2 or not W13.is_contiguous():
+            raise ValueError("W13 must be a contiguous [E, M, 2H] CUDA tensor")
+        self.E, self.M, self.H = W13.shape[0], W13.shape[1], W13.shape[2] // 2
+        self.C_max, self.act, self.device = C_max, W13.dtype, W13.device
+        check_tensor("W2", W2, (self.E, self.H, self.M), self.act, self.device)
+        self._keep = (W13, W2)
+        with torch.cuda.device(self.device):
+            self.h = L.moe_glu_create(self.E, C_max, self.M, self.H, self.act, ACTIVATIONS[activation], W13, W2)
+
+    def _rows(self, name, t, C=None):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [E, C, M]")
+        check_tensor(name, t, (self.E, t.shape[1] if C is None else C, self.M), self.act, self.device)
+        return t.shape[1]
+
+    def __call__(self, x: torch.Tensor, counts: torch.Tensor, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+        """y [E, C, M]: the experts' outputs for the rows they hold.  The other rows of `out`
+        stay as they are; of a new tensor they are unset."""
+        C = self._rows("x", x)
+        check_tensor("counts", counts, (self.E,), torch.int32, self.device)
+        if out is not None:
+            self._rows("out", out, C)
+        with on_stream(self.device, stream, x, counts, out) as st:
+            y = torch.empty_like(x) if out is None else out
+            L.moe_glu_forward(self.h, C, x, counts, y, st)
+        return y
+
+    def enable_backward(self) -> None:
+        """Allocate the backward's workspace; the forwards that follow keep g and u."""
+        with torch.cuda.device(self.device):
+            L.moe_glu_enable_backward(self.h)
+
+    def backward(self, x: torch.Tensor, counts: torch.Tensor, dy: torch.Tensor, out: dict | None = None,
+                 skip_empty_experts: bool = False, stream=None) -> dict:
+        """Gradients dx, dW13, dW2 for the last call (which took x and counts): new tensors, or
+        those of `out` (same keys) written in place.  dx has the rows the experts hold; with
+        skip_empty_experts the weight gradients of an expert without rows are left as they are."""
+        C = self._rows("x", x)
+        self._rows("dy", dy, C)
+        check_tensor("counts", counts, (self.E,), torch.int32, self.device)
+        out = dict(out or {})
+        shapes = {"dx": tuple(x.shape), "dW13": tuple(self._keep[0].shape), "dW2": tuple(self._keep[1].shape)}
+        for name, shape in shapes.items():
+            if out.get(name) is not None:
+                check_tensor(name, out[name], shape, self.act, self.device)
+        with on_stream(self.device, stream, x, counts, dy, *out.values()) as st:
+            g = {n: out[n] if out.get(n) is not None else torch.empty(s, dtype=self.act, device=self.device)
+                 for n, s in shapes.items()}
+            L.moe_glu_backward(self.h, C, x, counts, dy, g["dx"], g["dW13"], g["dW2"],
+                               L.MOE_BWD_SKIP_EMPTY_EXPERTS if skip_empty_experts else 0, st)
+        return g
+
+    def check(self, stream=None) -> None:
+        """Synchronise and raise a pending device error of this handle."""
+        with on_stream(self.device, stream) as st:
+            L.moe_glu_check(self.h, st)
+
+    def close(self) -> None:
+        if getattr(self, "h", None):
+            L.moe_glu_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

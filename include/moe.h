@@ -34,6 +34,7 @@
  *    on the next synchronising call (moe_aux_loss, moe_check) as MOE_ERR_CUDA or
  *    MOE_ERR_TIMEOUT.
  *  - A handle may be used by one host thread / one stream at a time.
+ *  - Beside the layer: gated experts on rows the caller has sorted by expert (moe_glu_*).
  */
 #ifndef GSHARD_MOE_H
 #define GSHARD_MOE_H
@@ -532,6 +533,72 @@ MOE_API moe_status moe_get_backward_stage_times(moe_handle h, float* ms_host, in
 
 /* Name of a MOE_BSTAGE_* index ("gate_bwd", "dW2", ...), or "?" */
 MOE_API const char* moe_backward_stage_name(int32_t stage);
+
+/* ---- gated experts ------------------------------------------------------------ */
+
+/*
+ * Gated feed-forward experts on rows that are already sorted by expert (the layer's
+ * dispatched buffers, or a caller's own; E = 1 is a dense gated feed-forward block):
+ *
+ *   g = x Wg, u = x Wu,  h = f(g) * u,  y = h W2           for the rows of each expert
+ *   dh = dy W2^T,  dg = dh * u * f'(g),  du = dh * f(g)
+ *   dx = dg Wg^T + du Wu^T,  dW13 = x^T [dg | du],  dW2 = h^T dy
+ *
+ * with W13 = [Wg | Wu] and f one of moe_glu_fn.  Both projections, f and the product are
+ * one kernel, and so are dh, dg and du.  Arithmetic is fp32 throughout (sums over the
+ * depth included); with bf16 the stored h, g, u, dg and du are rounded to bf16, as the
+ * operands of the products that follow, and so are the results.
+ *
+ * Rows: x, y, dy and dx are [E, C, M] act, and nrows_dev [E] int32 (device) says how many
+ * of its C rows each expert holds, read as min(max(nrows, 0), C).  Rows past that are not
+ * read as data (they may hold anything, NaN included) and not written.  C may differ from
+ * call to call, up to C_max.
+ */
+typedef struct moe_glu* moe_glu_handle;
+
+typedef enum {
+  MOE_GLU_SILU = 0,      /* f(g) = g / (1 + e^-g) */
+  MOE_GLU_GELU = 1,      /* f(g) = g (1 + erf(g / sqrt 2)) / 2 */
+  MOE_GLU_RELU = 2       /* f(g) = max(g, 0), f'(0) = 0 */
+} moe_glu_fn;
+
+/*
+ * moe_glu_create -- handle of E gated experts (1 .. 256) for up to C_max rows each
+ * (1 .. 2^21; E * round256(C_max) below 2^31, else MOE_ERR_UNSUPPORTED).  M, H: multiples
+ * of 64.  W13_dev [E, M, 2H] act (Wg in columns 0 .. H-1, Wu in H .. 2H-1), W2_dev
+ * [E, H, M] act: row-major, 16-byte aligned, borrowed until moe_glu_destroy.  One
+ * cudaMalloc (h, [E, round256(C_max), H] act); no later call allocates but
+ * moe_glu_enable_backward.  On error *out is NULL.
+ */
+MOE_API moe_status moe_glu_create(moe_glu_handle* out, int32_t E, int64_t C_max, int64_t M, int64_t H,
+                                  moe_dtype act, moe_glu_fn fn, const void* W13_dev, const void* W2_dev);
+MOE_API moe_status moe_glu_destroy(moe_glu_handle h);
+
+/* y of the rows each expert holds, enqueued on `stream`; no host synchronisation.  0 <= C <=
+ * C_max; x_dev and y_dev [E, C, M] act, 16-byte aligned, not overlapping. */
+MOE_API moe_status moe_glu_forward(moe_glu_handle h, int64_t C, const void* x_dev, const int32_t* nrows_dev,
+                                   void* y_dev, void* stream);
+
+/* Allocate the backward's workspace (once; a second call does nothing): [g | u] and
+ * [dg | du], each [E, round256(C_max), 2H] act.  The forwards that follow keep g and u.
+ * Synchronous (cudaMalloc); call it outside stream capture. */
+MOE_API moe_status moe_glu_enable_backward(moe_glu_handle h);
+
+/*
+ * moe_glu_backward -- gradients for the last moe_glu_forward of this handle (same C, same x
+ * and nrows, unchanged since), enqueued on `stream`; may run more than once per forward.
+ * dy_dev [E, C, M]; dx_dev [E, C, M] (rows each expert holds written), dW13_dev [E, M, 2H]
+ * and dW2_dev [E, H, M] overwritten, all act, 16-byte aligned, none overlapping another or
+ * an input.  An expert without rows gets zero weight gradients, or with
+ * MOE_BWD_SKIP_EMPTY_EXPERTS in `flags` none.  MOE_ERR_STATE unless that forward came after
+ * moe_glu_enable_backward.
+ */
+MOE_API moe_status moe_glu_backward(moe_glu_handle h, int64_t C, const void* x_dev, const int32_t* nrows_dev,
+                                    const void* dy_dev, void* dx_dev, void* dW13_dev, void* dW2_dev,
+                                    uint32_t flags, void* stream);
+
+/* Synchronise `stream` and report a pending device error of this handle (as moe_check). */
+MOE_API moe_status moe_glu_check(moe_glu_handle h, void* stream);
 
 /* Static description of a status code (never NULL). */
 MOE_API const char* moe_status_string(moe_status s);

@@ -139,3 +139,32 @@ def test_header_is_c11_and_links_from_c(tmp_path):
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0, (out.returncode, out.stderr)
     assert out.stdout.strip() == "ok 3"
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 8, 64, 64, 1, 0), 1),             # E = 0
+    ((8, 0, 64, 64, 1, 0), 1),             # C_max = 0
+    ((8, 8, 96, 64, 1, 0), 1),             # M not a multiple of 64
+    ((8, 8, 64, 100, 1, 0), 1),            # H not a multiple of 64
+    ((8, 8, 64, 64, 2, 0), 1),             # unknown activation type
+    ((8, 8, 64, 64, 1, 3), 1),             # unknown gate function
+    ((257, 8, 64, 64, 1, 0), 2),           # E > 256 unsupported
+    ((8, (1 << 21) + 1, 64, 64, 1, 0), 2),  # C_max > 2^21
+    ((8, 8, 1 << 17, 64, 1, 0), 2),
+])
+def test_gated_experts_reject_bad_arguments_before_device_work(L, args, status):
+    h = ctypes.c_void_p(123)
+    E, C, M, H, act, fn = args
+    assert L.lib.moe_glu_create(ctypes.byref(h), E, C, M, H, act, fn, FAKE, FAKE) == status
+    assert h.value is None
+    assert L.lib.moe_glu_create(ctypes.byref(h), 8, 8, 64, 64, 1, 0, FAKE + 8, FAKE) == 1
+    assert L.lib.moe_glu_create(ctypes.byref(h), 8, 8, 64, 64, 1, 0, FAKE, None) == 1
+    assert L.lib.moe_glu_create(None, 8, 8, 64, 64, 1, 0, FAKE, FAKE) == 1
+
+
+def test_gated_experts_null_handle_calls_are_rejected(L):
+    assert L.lib.moe_glu_forward(None, 1, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_glu_enable_backward(None) == 1
+    assert L.lib.moe_glu_backward(None, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == 1
+    assert L.lib.moe_glu_check(None, None) == 1
+    assert L.lib.moe_glu_destroy(None) == 0
