@@ -92,6 +92,12 @@ def _load() -> ctypes.CDLL:
         "moe_glu_enable_backward": [P],
         "moe_glu_backward": [P, I64, P, P, P, P, P, P, ctypes.c_uint32, P],
         "moe_glu_check": [P, P],
+        "moe_fp8_quantize_rows": [I64, I64, ctypes.c_int, P, P, P, P],
+        "moe_fp8_quantize_weights": [I32, I64, I64, ctypes.c_int, P, P, P, P],
+        "moe_fp8_create": [ctypes.POINTER(P), I32, I64, I64, I64, P, P],
+        "moe_fp8_destroy": [P],
+        "moe_fp8_matmul": [P, I64, P, P, P, P, P],
+        "moe_fp8_check": [P, P],
     })
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -418,3 +424,37 @@ def moe_glu_backward(h, C, x, nrows, dy, dx, dW13, dW2, flags=0, stream=None) ->
 
 def moe_glu_check(h, stream=None) -> None:
     _check("moe_glu_check", lib.moe_glu_check(h, _stream(stream)))
+
+
+# ---- 8-bit products with a scale for each block of 128
+
+def _src(dtype) -> int:
+    return MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+
+
+def moe_fp8_quantize_rows(R, K, x, q, s, stream=None) -> None:
+    _check("moe_fp8_quantize_rows", lib.moe_fp8_quantize_rows(R, K, _src(x.dtype), _ptr(x), _ptr(q), _ptr(s),
+                                                              _stream(stream)))
+
+
+def moe_fp8_quantize_weights(E, K, N, W, q, s, stream=None) -> None:
+    _check("moe_fp8_quantize_weights", lib.moe_fp8_quantize_weights(E, K, N, _src(W.dtype), _ptr(W), _ptr(q), _ptr(s),
+                                                                    _stream(stream)))
+
+
+def moe_fp8_create(E, C_max, K, N, wq, ws) -> int:
+    h = ctypes.c_void_p()
+    _check("moe_fp8_create", lib.moe_fp8_create(ctypes.byref(h), E, C_max, K, N, _ptr(wq), _ptr(ws)))
+    return h.value
+
+
+def moe_fp8_destroy(h) -> None:
+    _check("moe_fp8_destroy", lib.moe_fp8_destroy(h))
+
+
+def moe_fp8_matmul(h, C, xq, xs, nrows, y, stream=None) -> None:
+    _check("moe_fp8_matmul", lib.moe_fp8_matmul(h, C, _ptr(xq), _ptr(xs), _ptr(nrows), _ptr(y), _stream(stream)))
+
+
+def moe_fp8_check(h, stream=None) -> None:
+    _check("moe_fp8_check", lib.moe_fp8_check(h, _stream(stream)))

@@ -1,0 +1,315 @@
+// fp8.cu -- grouped 8-bit product with a scale for each block of 128 on tcgen05 (kind::f8f6f4):
+//
+//   y[m, n] = sum_kb xs[m, kb] ws[n / 128, kb] ( sum_{k in block kb} xq[m, k] wq[n, k] )
+//
+// for the rows m each expert holds.  The inner sum of a block is exact products added in
+// fp32 by the tensor cores into TMEM; the scales then enter once per block, in registers:
+// acc += (xs ws) * block.  So the tensor cores never accumulate across blocks, and the outer
+// sum is fp32 as well; y is rounded to bf16 once.
+//
+// A CTA pair (cta_group::2) computes 256 rows x 256 columns; CTA r holds rows [128r, +128) of
+// xq and columns [128r, +128) of wq, and all 256 columns of its rows in TMEM.  Two TMEM
+// buffers of 256 columns take turns: while the MMAs fill one with block kb + 1, eight warps
+// drain block kb from the other, each thread 128 columns of one row -- one row scale times
+// one column scale per block and thread -- into 128 registers.  320 threads: warp 0 loads
+// (TMA), warp 1 issues MMAs (the pair's first CTA) and owns TMEM, warps 2..9 drain.  Rows
+// past the count are neither read as data nor written; every wait is bounded.
+#include "common.cuh"
+#include "internal.h"
+#include "tc_tile.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BK = 128;                 // depth of a stage = of a scale block (bytes)
+constexpr int PM = 256, PN = 256;
+constexpr int kThreads = 320;
+constexpr int kDrain = 256;             // draining threads per CTA
+constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 5;
+constexpr uint32_t TMEM_COLS = 2 * PN;
+constexpr uint32_t TILE_BYTES = 4096;   // 32 rows x 64 bf16 columns
+constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;
+constexpr uint32_t kBars = 256;
+constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + 8 * TILE_BYTES + kBars + 16 + 4 * (3 * kMaxExperts + 1);
+static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+static_assert(SMEM + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
+
+struct Fp8Pair {
+  const int32_t* n;
+  int E, C, K, N, KB, NB;
+  const float* xs;       // [E, C, KB]
+  const float* ws;       // [E, NB, KB]
+  __nv_bfloat16* y;
+  unsigned* err;
+  uint64_t limit_ns;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmD, const Fp8Pair a) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
+  unsigned char* gbase = smem_raw + (base - raw_base);
+  const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
+  const uint32_t bar0 = tiles0 + 8 * TILE_BYTES;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
+  auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
+  const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + 8 * TILE_BYTES + kBars;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int* tile_pre = reinterpret_cast<int*>(misc + 16);   // [E + 1]
+  int* mtiles = tile_pre + (kMaxExperts + 1);          // [E]
+  int* nrows = mtiles + kMaxExperts;                   // [E]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int NT = (a.N + PN - 1) / PN;
+  const int KB = a.KB;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull_bar(i), 1);
+      mbar_init(tempty_bar(i), 2 * kDrain);     // draining threads of both CTAs
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (warp == 2) {
+    const int per = (a.E + 31) / 32;
+    const int e0 = lane * per;
+    int sum = 0;
+    for (int e = e0; e < min(a.E, e0 + per); ++e) {
+      nrows[e] = min(max(a.n[e], 0), a.C);
+      mtiles[e] = (nrows[e] + PM - 1) / PM;
+      sum += mtiles[e] * NT;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int run = inc - sum;
+    for (int e = e0; e < min(a.E, e0 + per); ++e) {
+      tile_pre[e] = run;
+      run += mtiles[e] * NT;
+    }
+    if (lane == 31) tile_pre[a.E] = inc;
+  }
+  tc_fence_before();
+  cluster_sync_all();          // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      TileIter it{tile_pre, mtiles, a.E, NT, 0};
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int e, mt, nt;
+      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+        const int rowA = e * a.C + mt * PM + (int)rank * 128;
+        const int rowB = e * a.N + nt * PN + (int)rank * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t fb = full_bar(s) & kPeerBitMask;
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          // depth past K (a last block cut short) reads as zeros
+          tma_load_2d_pair(sa, &tmA, fb, kb * BK, rowA);
+          tma_load_2d_pair(sa + A_BYTES, &tmB, fb, kb * BK, rowB);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (lane == 0 && leader) {
+      TileIter it{tile_pre, mtiles, a.E, NT, 0};
+      // kind::f8f6f4, D fp32, A and B e4m3 (0) with contiguous depth, M = 256, N = 256
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      int e, mt, nt;
+      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (*abort_flag || !mbar_wait(tempty_bar(acc), aph ^ 1u, a.err, a.limit_ns) ||
+              !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + s * STAGE_BYTES;
+          const uint32_t d_tmem = tmem_base + acc * PN;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            tc_mma_f8_pair(d_tmem, desc_sw128(sa + kk * 32u, 16u, 1024u), desc_sw128(sa + A_BYTES + kk * 32u, 16u, 1024u),
+                           idesc, kk != 0);
+          tc_commit_pair(empty_bar(s), 0x3);
+          tc_commit_pair(tfull_bar(acc), 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+          acc ^= 1;
+          if (acc == 0) aph ^= 1u;
+        }
+      }
+      if (!ok) {
+        tc_commit_pair(done_bar, 0x1);
+        mbar_wait(done_bar, 0, a.err, a.limit_ns);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ drain (warps 2..9, both CTAs)
+    const int q = warp & 3;                        // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;              // its 128 of the tile's 256 columns
+    const uint32_t tile0 = tiles0 + (warp - 2) * TILE_BYTES;
+    TileIter it{tile_pre, mtiles, a.E, NT, 0};
+    int e, mt, nt, acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+      const int local = mt * PM + (int)rank * 128 + q * 32;
+      const int nvalid = min(32, nrows[e] - local);
+      const int64_t row0 = (int64_t)e * a.C + local;
+      const int col0 = nt * PN + half * 128;
+      const int nb = nt * 2 + half;
+      const bool live = lane < nvalid && nb < a.NB;
+      const float* xs = a.xs + (row0 + (live ? lane : 0)) * KB;
+      const float* ws = a.ws + ((int64_t)e * a.NB + (live ? nb : 0)) * KB;
+      float sum[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+      float sc = live ? __ldg(xs) * __ldg(ws) : 0.f;
+      for (int kb = 0; kb < KB; ++kb) {
+        const float scn = live && kb + 1 < KB ? __ldg(xs + kb + 1) * __ldg(ws + kb + 1) : 0.f;
+        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (nvalid > 0) {
+          const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + half * 128;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tm + c * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] = fmaf(sc, __uint_as_float(r[j]), sum[c * 32 + j]);
+          }
+        }
+        tc_fence_before();
+        if (leader) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+        sc = scn;
+      }
+      if (ok && nvalid > 0) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int col = col0 + b * 64;
+          if (col < a.N) {
+            if (nvalid == 32) {
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(sum[b * 64 + j * 8 + 2 * i], sum[b * 64 + j * 8 + 2 * i + 1]);
+              if (nvalid == 32)
+                st_shared_v4(tile0 + lane * 128 + ((j ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+              else if (lane < nvalid && col + j * 8 < a.N)       // N is a multiple of 8
+                *reinterpret_cast<uint4*>(a.y + (row0 + lane) * a.N + col + j * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            if (nvalid == 32) {
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d_hint(&tmD, tile0, col, (int)row0, l2_policy_evict_first());
+                bulk_commit();
+              }
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();          // no CTA leaves while its pair may still use its smem or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+cudaError_t fp8_matmul(const Fp8Args& a) {
+  CUtensorMap tmA, tmB, tmD;
+  const uint64_t rows = (uint64_t)a.E * (uint64_t)a.C;
+  if (!encode_2d_bytes(&tmA, a.xq, a.K, rows, BK, 128) || !encode_2d_bytes(&tmB, a.wq, a.K, (uint64_t)a.E * a.N, BK, 128) ||
+      !encode_2d(&tmD, a.y, a.N, rows, 64, 32))
+    return cudaErrorInvalidValue;
+  Fp8Pair p{};
+  p.n = a.n;
+  p.E = a.E;
+  p.C = (int)a.C;
+  p.K = a.K;
+  p.N = a.N;
+  p.KB = (a.K + 127) / 128;
+  p.NB = (a.N + 127) / 128;
+  p.xs = a.xs;
+  p.ws = a.ws;
+  p.y = static_cast<__nv_bfloat16*>(a.y);
+  p.err = a.err;
+  p.limit_ns = a.limit_ns;
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fp8_pair_kernel, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
+}
+
+}  // namespace moe

@@ -46,6 +46,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // 0 = dense), bf16 or fp32, 128-byte swizzle.
 bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in,
                uint32_t box_out, bool f32 = false, uint64_t pitch = 0);
+// The same of bytes (8-bit values), dense.
+bool encode_2d_bytes(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in, uint32_t box_out);
 
 // Device tables of one forward (all owned by the handle's workspace).
 struct Routing {
@@ -295,6 +297,25 @@ cudaError_t glu_dh_f32(const GluArgs& a);
 cudaError_t glu_dx_f32(const GluArgs& a);
 cudaError_t glu_dw2_f32(const GluArgs& a);
 cudaError_t glu_dw13_f32(const GluArgs& a);
+// 8-bit products with a scale for each block of 128 (fp8.cu): y = (xq * xs) (wq * ws)^T
+struct Fp8Args {
+  int E, K, N;
+  int64_t C;             // rows per expert of xq, xs, y
+  const int32_t* n;      // [E] device: rows each expert holds, read as min(max(n, 0), C)
+  const void* xq;        // [E, C, K] e4m3
+  const float* xs;       // [E, C, ceil(K/128)]
+  const void* wq;        // [E, N, K] e4m3
+  const float* ws;       // [E, ceil(N/128), ceil(K/128)]
+  void* y;               // [E, C, N] bf16
+  unsigned* err;
+  uint64_t limit_ns;
+  int num_sms;
+  cudaStream_t st;
+};
+cudaError_t fp8_matmul(const Fp8Args& a);
+// fp8_quantize.cu
+cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* q, float* s, cudaStream_t st);
+cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st);
 // selftest.cu
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st);
 

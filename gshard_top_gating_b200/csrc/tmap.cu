@@ -41,4 +41,8 @@ bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer,
                 inner, outer, box_in, box_out, pitch);
 }
 
+bool encode_2d_bytes(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in, uint32_t box_out) {
+  return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, inner, outer, box_in, box_out, 0);
+}
+
 }  // namespace moe

@@ -118,7 +118,8 @@ class GatedExperts:
 
     def close(self) -> None:
         if getattr(self, "h", None):
-            L.moe_glu_destroy(self.h)
+            with torch.cuda.device(self.device):
+                L.moe_glu_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -34,7 +34,8 @@
  *    on the next synchronising call (moe_aux_loss, moe_check) as MOE_ERR_CUDA or
  *    MOE_ERR_TIMEOUT.
  *  - A handle may be used by one host thread / one stream at a time.
- *  - Beside the layer: gated experts on rows the caller has sorted by expert (moe_glu_*).
+ *  - Beside the layer: gated experts on rows the caller has sorted by expert (moe_glu_*),
+ *    and 8-bit products with a scale for each block of 128 (moe_fp8_*).
  */
 #ifndef GSHARD_MOE_H
 #define GSHARD_MOE_H
@@ -599,6 +600,58 @@ MOE_API moe_status moe_glu_backward(moe_glu_handle h, int64_t C, const void* x_d
 
 /* Synchronise `stream` and report a pending device error of this handle (as moe_check). */
 MOE_API moe_status moe_glu_check(moe_glu_handle h, void* stream);
+
+/* ---- 8-bit products with a scale for each block of 128 -------------------------- */
+
+/*
+ * Values in e4m3 (8-bit floating point, largest 448) with one fp32 scale per block: rows
+ * of activations in blocks of 1 x 128 along the depth, weights in blocks of 128 x 128; a
+ * last block may be cut short.  A value stands for q * s of its block.
+ */
+
+/*
+ * moe_fp8_quantize_rows -- q_dev [R, K] e4m3 and s_dev [R, ceil(K/128)] fp32 of x_dev [R, K]
+ * (MOE_BF16 or MOE_F32, row-major): per block a = max(max|x|, 2^-100), s = a / 448,
+ * q = x * (448 / a) rounded to nearest even.  A block with a NaN becomes all NaN, one with
+ * an infinity has an infinite scale.  K: a multiple of 16; x and q 16-byte aligned;
+ * R * ceil(K/128) below 2^31.  Enqueued on `stream`.
+ */
+MOE_API moe_status moe_fp8_quantize_rows(int64_t R, int64_t K, moe_dtype src, const void* x_dev, void* q_dev,
+                                         float* s_dev, void* stream);
+
+/*
+ * moe_fp8_quantize_weights -- the same for expert weights, with the layer's layout as input:
+ * W_dev [E, K, N] -> q_dev [E, N, K] (depth contiguous) and s_dev [E, ceil(N/128),
+ * ceil(K/128)], one scale per 128 x 128 block.  K: a multiple of 16, N: of 8.
+ */
+MOE_API moe_status moe_fp8_quantize_weights(int32_t E, int64_t K, int64_t N, moe_dtype src, const void* W_dev,
+                                            void* q_dev, float* s_dev, void* stream);
+
+typedef struct moe_fp8* moe_fp8_handle;
+
+/*
+ * moe_fp8_create -- handle of a grouped product y[e] = x[e] w[e]^T of E experts (1 .. 256; 1 is
+ * a plain product) for up to C_max rows each (1 .. 2^21).  wq_dev [E, N, K] e4m3 and ws_dev
+ * [E, ceil(N/128), ceil(K/128)] are borrowed until moe_fp8_destroy.  K: a multiple of 16,
+ * N: of 8.  One cudaMalloc; no later call allocates.  On error *out is NULL.
+ */
+MOE_API moe_status moe_fp8_create(moe_fp8_handle* out, int32_t E, int64_t C_max, int64_t K, int64_t N,
+                                  const void* wq_dev, const float* ws_dev);
+MOE_API moe_status moe_fp8_destroy(moe_fp8_handle h);
+
+/*
+ * moe_fp8_matmul -- y_dev [E, C, N] bf16 of xq_dev [E, C, K] e4m3 and xs_dev [E, C,
+ * ceil(K/128)], for the rows each expert holds (nrows_dev [E] int32, device, read as
+ * min(max(nrows, 0), C)); the other rows are not read as data and not written.
+ *   y[m, n] = sum_kb xs[m, kb] ws[n / 128, kb] (sum_{k in kb} xq[m, k] wq[n, k])
+ * with all sums in fp32 and one rounding to bf16.  0 <= C <= C_max; 16-byte aligned.
+ * Enqueued on `stream`, no host synchronisation.
+ */
+MOE_API moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq_dev, const float* xs_dev,
+                                  const int32_t* nrows_dev, void* y_dev, void* stream);
+
+/* Synchronise `stream` and report a pending device error of this handle (as moe_check). */
+MOE_API moe_status moe_fp8_check(moe_fp8_handle h, void* stream);
 
 /* Static description of a status code (never NULL). */
 MOE_API const char* moe_status_string(moe_status s);

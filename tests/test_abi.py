@@ -168,3 +168,35 @@ def test_gated_experts_null_handle_calls_are_rejected(L):
     assert L.lib.moe_glu_backward(None, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == 1
     assert L.lib.moe_glu_check(None, None) == 1
     assert L.lib.moe_glu_destroy(None) == 0
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 8, 64, 64), 1),                   # E = 0
+    ((8, 0, 64, 64), 1),                   # C_max = 0
+    ((8, 8, 72, 64), 1),                   # K not a multiple of 16
+    ((8, 8, 64, 60), 1),                   # N not a multiple of 8
+    ((257, 8, 64, 64), 2),
+    ((8, (1 << 21) + 1, 64, 64), 2),
+    ((8, 8, (1 << 20) + 16, 64), 2),
+])
+def test_fp8_product_rejects_bad_arguments_before_device_work(L, args, status):
+    h = ctypes.c_void_p(123)
+    assert L.lib.moe_fp8_create(ctypes.byref(h), *args, FAKE, FAKE) == status
+    assert h.value is None
+    assert L.lib.moe_fp8_create(ctypes.byref(h), 8, 8, 64, 64, FAKE + 8, FAKE) == 1
+    assert L.lib.moe_fp8_create(ctypes.byref(h), 8, 8, 64, 64, FAKE, None) == 1
+    assert L.lib.moe_fp8_create(None, 8, 8, 64, 64, FAKE, FAKE) == 1
+
+
+def test_fp8_calls_are_rejected_before_device_work(L):
+    assert L.lib.moe_fp8_matmul(None, 1, FAKE, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_check(None, None) == 1
+    assert L.lib.moe_fp8_destroy(None) == 0
+    assert L.lib.moe_fp8_quantize_rows(1, 24, 1, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_quantize_rows(-1, 32, 1, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_quantize_rows(1, 32, 2, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_quantize_rows(1, 32, 1, FAKE + 4, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_quantize_rows(1 << 31, 32, 1, FAKE, FAKE, FAKE, None) == 2
+    assert L.lib.moe_fp8_quantize_rows(0, 32, 1, None, None, None, None) == 0
+    assert L.lib.moe_fp8_quantize_weights(1, 32, 12, 1, FAKE, FAKE, FAKE, None) == 1
+    assert L.lib.moe_fp8_quantize_weights(0, 32, 16, 1, FAKE, FAKE, FAKE, None) == 1
