@@ -11,9 +11,11 @@
 // xq and columns [128r, +128) of wq, and all 256 columns of its rows in TMEM.  Two TMEM
 // buffers of 256 columns take turns: while the MMAs fill one with block kb + 1, eight warps
 // drain block kb from the other, each thread 128 columns of one row -- one row scale times
-// one column scale per block and thread -- into 128 registers.  320 threads: warp 0 loads
-// (TMA), warp 1 issues MMAs (the pair's first CTA) and owns TMEM, warps 2..9 drain.  Rows
-// past the count are neither read as data nor written; every wait is bounded.
+// one column scale per block and thread -- into 128 registers.  Warp 0 loads (TMA),
+// warp 1 issues MMAs (the pair's first CTA) and owns TMEM, warps 4..11 drain.  A buffer is
+// handed back as soon as its last column is in registers, by one arrival per warp (the second
+// CTA's arrivals cross to the first).  Rows past the count are neither read as data nor
+// written; every wait is bounded.
 #include "common.cuh"
 #include "internal.h"
 #include "tc_tile.cuh"
@@ -24,8 +26,10 @@ namespace {
 
 constexpr int BK = 128;                 // depth of a stage = of a scale block (bytes)
 constexpr int PM = 256, PN = 256;
-constexpr int kThreads = 320;
-constexpr int kDrain = 256;             // draining threads per CTA
+constexpr int kThreads = 384;           // loads, MMAs and two idle warps; eight draining warps
+constexpr int kDrainWarps = 8;
+// Registers: 384 threads launch with 168 each (64,512); 128 keep 72, 256 take 216 (the same).
+constexpr int kRegsLoad = 72, kRegsDrain = 216;
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 5;
 constexpr uint32_t TMEM_COLS = 2 * PN;
@@ -81,7 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 2 * kDrain);     // draining threads of both CTAs
+      mbar_init(tempty_bar(i), 2 * kDrainWarps);   // draining warps of both CTAs
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -122,6 +126,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  if (warp < 4) {
+    reg_dec<kRegsLoad>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
@@ -173,13 +179,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t sa = base + s * STAGE_BYTES;
-          const uint32_t d_tmem = tmem_base + acc * PN;
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            tc_mma_f8_pair(d_tmem, desc_sw128(sa + kk * 32u, 16u, 1024u), desc_sw128(sa + A_BYTES + kk * 32u, 16u, 1024u),
-                           idesc, kk != 0);
-          tc_commit_pair(empty_bar(s), 0x3);
+            tc_mma_f8_pair(tmem_base + acc * PN, desc_sw128(sa + kk * 32u, 16u, 1024u),
+                           desc_sw128(sa + A_BYTES + kk * 32u, 16u, 1024u), idesc, kk != 0);
           tc_commit_pair(tfull_bar(acc), 0x3);
+          tc_commit_pair(empty_bar(s), 0x3);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
@@ -194,11 +199,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  }
   } else {
-    // ------------------------------------------------------------ drain (warps 2..9, both CTAs)
+    // ------------------------------------------------------------ drain (warps 4..11, both CTAs)
+    reg_inc<kRegsDrain>();
     const int q = warp & 3;                        // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;              // its 128 of the tile's 256 columns
-    const uint32_t tile0 = tiles0 + (warp - 2) * TILE_BYTES;
+    const int half = (warp - 4) >> 2;              // its 128 of the tile's 256 columns
+    const uint32_t tile0 = tiles0 + (warp - 4) * TILE_BYTES;
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, acc = 0;
     uint32_t aph = 0;
@@ -215,32 +222,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float sum[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0.f;
-      float sc = live ? __ldg(xs) * __ldg(ws) : 0.f;
-      for (int kb = 0; kb < KB; ++kb) {
-        const float scn = live && kb + 1 < KB ? __ldg(xs + kb + 1) * __ldg(ws + kb + 1) : 0.f;
+      auto scale = [&](int kb, float& x, float& w) {
+        x = live && kb < KB ? __ldg(xs + kb) : 0.f;
+        w = live && kb < KB ? __ldg(ws + kb) : 0.f;
+      };
+      // adds block kb; its scales were loaded two blocks ago, those of block kb + 2 are now
+      auto drain = [&](int kb, float& x, float& w) -> bool {
         if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
           *abort_flag = 1;
-          ok = false;
-          break;
+          return false;
         }
         tc_fence_after();
-        if (nvalid > 0) {
-          const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + half * 128;
+        const float sc = x * w;
+        scale(kb + 2, x, w);
+        const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + half * 128;
+        uint32_t r[2][32];
+        if (nvalid > 0) tmem_ld_32x32b_x32(tm, r[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tm + c * 32, r);
+        for (int c = 0; c < 4; ++c) {
+          if (nvalid > 0) {
             tmem_ld_wait();
+            if (c < 3) tmem_ld_32x32b_x32(tm + (c + 1) * 32, r[(c + 1) & 1]);
+          }
+          if (c == 3) {                   // the buffer's last column is here: hand it back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (leader) mbar_arrive(tempty_bar(acc));
+              else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
+            }
+          }
+          if (nvalid > 0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[c * 32 + j] = fmaf(sc, __uint_as_float(r[j]), sum[c * 32 + j]);
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] = fmaf(sc, __uint_as_float(r[c & 1][j]), sum[c * 32 + j]);
           }
         }
-        tc_fence_before();
-        if (leader) mbar_arrive(tempty_bar(acc));
-        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
-        sc = scn;
+        return true;
+      };
+      float x0, w0, x1, w1;
+      scale(0, x0, w0);
+      scale(1, x1, w1);
+      for (int kb = 0; ok && kb < KB; kb += 2) {
+        ok = drain(kb, x0, w0);
+        if (ok && kb + 1 < KB) ok = drain(kb + 1, x1, w1);
       }
       if (ok && nvalid > 0) {
 #pragma unroll
