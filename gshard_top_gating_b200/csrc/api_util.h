@@ -39,14 +39,15 @@ inline bool on_device(int device) {
   return cudaGetDevice(&cur) == cudaSuccess && cur == device;
 }
 
-// Synchronises `st`, reads a device error word and clears it.
-inline moe_status take_device_error(unsigned* err, cudaStream_t st) {
+// Synchronises `st`, reads a device error word and, if it is set, clears it and the words
+// behind it (`words` in all).
+inline moe_status take_device_error(unsigned* err, cudaStream_t st, size_t words = 1) {
   unsigned e = 0;
   cudaError_t ce = cudaMemcpyAsync(&e, err, sizeof(unsigned), cudaMemcpyDeviceToHost, st);
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
   if (ce != cudaSuccess) return status_of(ce);
   if (!e) return MOE_OK;
-  ce = cudaMemsetAsync(err, 0, sizeof(unsigned), st);
+  ce = cudaMemsetAsync(err, 0, words * sizeof(unsigned), st);
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
   if (ce != cudaSuccess) return status_of(ce);
   return (e & DEVERR_TIMEOUT) ? MOE_ERR_TIMEOUT : MOE_ERR_CUDA;

@@ -12,6 +12,10 @@ struct moe_fp8 {
   const void* wq;
   const float* ws;
   int device, num_sms;
+  void* ws_dev;          // the handle's allocation
+  float* part;           // few_rows.cu: partial sums, arrival counts
+  unsigned* count;
+  size_t ncount;
   unsigned* err;
 };
 
@@ -52,11 +56,21 @@ moe_status moe_fp8_create(moe_fp8_handle* out, int32_t E, int64_t C_max, int64_t
   h->ws = ws;
   cudaError_t ce = cudaGetDevice(&h->device);
   if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
-  if (ce == cudaSuccess) ce = cudaMalloc(&h->err, 256);
-  if (ce == cudaSuccess) ce = cudaMemset(h->err, 0, 256);
+  BufferCarver c{nullptr};
+  for (int pass = 0; ce == cudaSuccess && pass < 2; ++pass) {
+    c.off = 0;
+    h->part = c.take<float>(few_rows_workspace(C_max, true, h->num_sms, &h->ncount));
+    h->err = c.take<unsigned>(1 + h->ncount);     // the error word, then the counts
+    h->count = h->err + 1;
+    if (pass == 0) {
+      ce = cudaMalloc(&h->ws_dev, c.off + 256);
+      c.base = static_cast<char*>(h->ws_dev);
+    }
+  }
+  if (ce == cudaSuccess) ce = cudaMemset(h->err, 0, (1 + h->ncount) * sizeof(unsigned));
   if (ce != cudaSuccess) {
     cudaGetLastError();
-    if (h->err) cudaFree(h->err);
+    if (h->ws_dev) cudaFree(h->ws_dev);
     delete h;
     return status_of(ce);
   }
@@ -67,14 +81,14 @@ moe_status moe_fp8_create(moe_fp8_handle* out, int32_t E, int64_t C_max, int64_t
 moe_status moe_fp8_destroy(moe_fp8_handle h) {
   if (!h) return MOE_OK;
   cudaError_t ce = cudaDeviceSynchronize();
-  const cudaError_t fe = cudaFree(h->err);
+  const cudaError_t fe = cudaFree(h->ws_dev);
   delete h;
   return status_of(ce != cudaSuccess ? ce : fe);
 }
 
 moe_status moe_fp8_check(moe_fp8_handle h, void* stream) {
   if (!h || !on_device(h->device)) return MOE_ERR_INVALID_ARG;
-  return take_device_error(h->err, static_cast<cudaStream_t>(stream));
+  return take_device_error(h->err, static_cast<cudaStream_t>(stream), 1 + h->ncount);
 }
 
 moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq, const float* xs, const int32_t* nrows, void* y,
@@ -95,11 +109,13 @@ moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq, const flo
   a.wq = h->wq;
   a.ws = h->ws;
   a.y = y;
+  a.part = h->part;
+  a.count = h->count;
   a.err = h->err;
   a.limit_ns = 2000000000ull;   // 2 s per wait: far above any legitimate one
   a.num_sms = h->num_sms;
   a.st = static_cast<cudaStream_t>(stream);
-  return status_of(fp8_matmul(a));
+  return status_of(C <= 64 ? fp8_few(a) : fp8_matmul(a));
 }
 
 }  // extern "C"

@@ -17,6 +17,9 @@ struct moe_glu {
   const void* W2;
   void* ws;
   void* h;               // [E, Cp, H] act
+  float* part;           // few_rows.cu: partial sums, arrival counts
+  unsigned* count;
+  size_t ncount;
   unsigned* err;
   void* bws;             // the backward's allocation (moe_glu_enable_backward)
   void* gu;              // [E, Cp, 2H] act
@@ -47,6 +50,8 @@ GluArgs args_of(moe_glu_handle h, int64_t C, const void* x, const int32_t* n, cu
   a.dgu = h->dgu;
   a.tx = h->tx;
   a.tdy = h->tdy;
+  a.part = h->part;
+  a.count = h->count;
   a.err = h->err;
   a.limit_ns = kWaitLimitNs;
   a.num_sms = h->num_sms;
@@ -93,13 +98,18 @@ moe_status moe_glu_create(moe_glu_handle* out, int32_t E, int64_t C_max, int64_t
   for (int pass = 0; ce == cudaSuccess && pass < 2; ++pass) {
     c.off = 0;
     h->h = c.take<char>((size_t)E * Cp * H * act_bytes_of(act));
-    h->err = c.take<unsigned>(1);
+    if (act == MOE_BF16) {
+      const size_t parts = few_rows_workspace(C_max, false, h->num_sms, &h->ncount);
+      h->part = c.take<float>(parts);
+    }
+    h->err = c.take<unsigned>(1 + h->ncount);     // the error word, then the counts
+    h->count = h->err + 1;
     if (pass == 0) {
       ce = cudaMalloc(&h->ws, c.off + 256);
       c.base = static_cast<char*>(h->ws);
     }
   }
-  if (ce == cudaSuccess) ce = cudaMemset(h->err, 0, sizeof(unsigned));
+  if (ce == cudaSuccess) ce = cudaMemset(h->err, 0, (1 + h->ncount) * sizeof(unsigned));
   if (ce != cudaSuccess) {
     cudaGetLastError();
     if (h->ws) cudaFree(h->ws);
@@ -122,7 +132,7 @@ moe_status moe_glu_destroy(moe_glu_handle h) {
 
 moe_status moe_glu_check(moe_glu_handle h, void* stream) {
   if (!h || !on_device(h->device)) return MOE_ERR_INVALID_ARG;
-  return take_device_error(h->err, static_cast<cudaStream_t>(stream));
+  return take_device_error(h->err, static_cast<cudaStream_t>(stream), 1 + h->ncount);
 }
 
 moe_status moe_glu_enable_backward(moe_glu_handle h) {
@@ -164,7 +174,10 @@ moe_status moe_glu_forward(moe_glu_handle h, int64_t C, const void* x, const int
   if (C > 0) {
     GluArgs a = args_of(h, C, x, nrows, static_cast<cudaStream_t>(stream));
     a.y = y;
-    if (h->act == MOE_BF16) {
+    if (h->act == MOE_BF16 && C <= 128) {
+      GLU_TRY(glu_few_up(a));
+      GLU_TRY(glu_few_down(a));
+    } else if (h->act == MOE_BF16) {
       GLU_TRY(glu_up_bf16(a));
       GLU_TRY(glu_down_bf16(a));
     } else {

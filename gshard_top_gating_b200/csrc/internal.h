@@ -279,6 +279,8 @@ struct GluArgs {
   void* tx;              // bf16: [E, 64, M] copies of the last partial 64-row block of x and of
   void* tdy;             //   dy, or null where those rows hold zeros up to a multiple of 64
   bool skip_empty;       // experts without rows leave dW13[e], dW2[e] as they are (else zeros)
+  float* part;           // few_rows.cu: partial sums and arrival counts (few_rows_workspace)
+  unsigned* count;
   unsigned* err;
   uint64_t limit_ns;
   int num_sms;
@@ -307,12 +309,21 @@ struct Fp8Args {
   const void* wq;        // [E, N, K] e4m3
   const float* ws;       // [E, ceil(N/128), ceil(K/128)]
   void* y;               // [E, C, N] bf16
+  float* part;           // few_rows.cu: partial sums and arrival counts (few_rows_workspace)
+  unsigned* count;
   unsigned* err;
   uint64_t limit_ns;
   int num_sms;
   cudaStream_t st;
 };
 cudaError_t fp8_matmul(const Fp8Args& a);
+// few_rows.cu: the same products (gated experts' up and down in bf16, the 8-bit one) for few
+// rows.  Workspace: floats of partial sums (returned) and counts, zero before the first
+// launch; every launch leaves the counts zero.
+size_t few_rows_workspace(int64_t C_max, bool fp8, int num_sms, size_t* counts);
+cudaError_t glu_few_up(const GluArgs& a);
+cudaError_t glu_few_down(const GluArgs& a);
+cudaError_t fp8_few(const Fp8Args& a);
 // fp8_quantize.cu
 cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* q, float* s, cudaStream_t st);
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st);

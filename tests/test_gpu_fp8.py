@@ -130,6 +130,10 @@ CASES = [
     (3, 40, 112, 72, [-5, 1000, 31]),        # counts outside [0, C] are clamped
     (256, 2, 128, 16, [i % 3 for i in range(256)]),
     (3, 600, 7168, 256, [511, 0, 600]),
+    (4, 17, 7168, 520, [17, 0, 1, 16]),
+    (16, 64, 2048, 384, [64, 33, 0, 1] * 4),
+    (1, 1, 4096, 1024, [1]),
+    (2, 30, 1168, 264, [30, 19]),
 ]
 
 

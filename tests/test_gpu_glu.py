@@ -13,6 +13,9 @@ Norm: the roundings of independent elements do not add up, so the Frobenius norm
 error is at most u times the number of roundings on the way (y: h and y; dW2: h and dW2;
 dx and dW13: g and u, dg and du, the result, and one for the product of two rounded
 factors), relative to the norm of the result; fp32 4 * 2^-24 * sqrt(depth) likewise.
+With ReLU, dg of an element whose |g| is within its own error (K 2^-23 sum |x w|, and u |g|)
+may be dh u or 0; the two differ by |dh u|, so the norm of those elements' part of dx and of
+dW13, sum |dh u| |Wg| and sum |x| |dh u|, is allowed on top.
 """
 from __future__ import annotations
 
@@ -89,7 +92,10 @@ def reference(x, dy, W13, W2, n, fn):
         dW2 = h.T @ D
         e2 = (eh + k * h.abs()).T @ D.abs()
         e2 = e2 + u * (dW2.abs() + e2)
-        res.append(dict(r=r, y=(y, ey), dx=(dx, edx), dW13=(dW13, e13), dW2=(dW2, e2)))
+        amb = edf * (dh * v).abs() if fn == "relu" else torch.zeros_like(dg)
+        s13 = torch.cat([X.abs().T @ amb, torch.zeros_like(X.T @ du)], 1)
+        res.append(dict(r=r, y=(y, ey, 0.0), dx=(dx, edx, float((amb @ Wg.abs().T).norm())), dW13=(dW13, e13, float(s13.norm())),
+                        dW2=(dW2, e2, 0.0)))
     return res
 
 
@@ -97,15 +103,14 @@ ROUNDINGS = {"y": 2, "dW2": 2, "dx": 4, "dW13": 4}
 
 
 def check(name, got, ref, dtype, depth):
-    val, err = ref
+    val, err, flips = ref
     d = (got.double() - val).abs()
     tiny = 1e-30
     assert bool(torch.isfinite(got.double()).all()), name
     assert bool((d <= err + tiny).all()), (name, float((d - err).max()))
     if val.numel():
         bar = ROUNDINGS[name] * U[dtype] * (math.sqrt(depth) if dtype == torch.float32 else 1.0)
-        rel = float(d.norm() / val.norm().clamp(min=tiny))
-        assert rel <= bar, (name, rel, bar)
+        assert float(d.norm()) <= bar * float(val.norm()) + flips + tiny, (name, float(d.norm()), float(val.norm()), bar, flips)
 
 
 CASES = [
@@ -121,6 +126,10 @@ CASES = [
     (3, 600, 512, 256, [511, 0, 513]),
     (3, 40, 64, 64, [-5, 1000, 31]),          # counts outside [0, C] are clamped
     (256, 2, 64, 64, [i % 3 for i in range(256)]),
+    (8, 20, 1024, 1088, [0, 1, 20, 17, 0, 16, 3, 2]),
+    (32, 1, 512, 1024, [int(i in (9, 13)) for i in range(32)]),
+    (3, 100, 576, 704, [100, 64, 1]),
+    (2, 128, 192, 1216, [128, 33]),
 ]
 
 
@@ -162,6 +171,9 @@ def test_forward_and_backward(case, fn, dtype):
 def test_inference_equals_training_forward(dtype):
     x, dy, W13, W2, n = make(4, 300, 128, 384, dtype, [300, 17, 0, 256])
     a, b = experts(300, W13, W2, "silu", backward=False), experts(512, W13, W2, "silu")
+    ya, yb = torch.zeros_like(x), torch.zeros_like(x)
+    assert torch.equal(a(x, n, out=ya), b(x, n, out=yb))
+    x, n = x[:, :40].contiguous(), n.clamp(max=39)
     ya, yb = torch.zeros_like(x), torch.zeros_like(x)
     assert torch.equal(a(x, n, out=ya), b(x, n, out=yb))
 
