@@ -24,32 +24,26 @@ def check_tensor(name, t, shape, dtype, device) -> None:
                          f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
-class on_stream:
-    """Context of one call: the handle's device current and `stream` (default: that device's
-    current stream) the one that new tensors are allocated on; tensors of other streams
-    that the call uses are recorded on it."""
-
-    def __init__(self, device, stream, *tensors):
+def launch_on(device, stream, tensors, call):
+    """call(raw stream) with the operator's device current and `stream` (default: that device's
+    current stream) the one that new tensors are allocated on; tensors of other streams that
+    the call uses are recorded on it."""
+    if stream is None and torch.cuda.current_device() == device.index:     # the usual call, without contexts
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        current = torch.cuda.current_stream(device)
         if stream is None:
-            stream = torch.cuda.current_stream(device)
+            stream = current
         elif isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the operator on {device}")
-        self.stream, self.tensors = stream, tensors
-        self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        other = self.stream != torch.cuda.current_stream(self.stream.device)
-        self.ctx.__enter__()
-        if other:
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+        with torch.cuda.stream(stream):
+            if stream != current:
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+            return call(stream.cuda_stream)
 
 
 class GatedExperts:
@@ -81,10 +75,12 @@ class GatedExperts:
         check_tensor("counts", counts, (self.E,), torch.int32, self.device)
         if out is not None:
             self._rows("out", out, C)
-        with on_stream(self.device, stream, x, counts, out) as st:
+
+        def call(st):
             y = torch.empty_like(x) if out is None else out
             L.moe_glu_forward(self.h, C, x, counts, y, st)
-        return y
+            return y
+        return launch_on(self.device, stream, (x, counts, out), call)
 
     def enable_backward(self) -> None:
         """Allocate the backward's workspace; the forwards that follow keep g and u."""
@@ -104,17 +100,18 @@ class GatedExperts:
         for name, shape in shapes.items():
             if out.get(name) is not None:
                 check_tensor(name, out[name], shape, self.act, self.device)
-        with on_stream(self.device, stream, x, counts, dy, *out.values()) as st:
+
+        def call(st):
             g = {n: out[n] if out.get(n) is not None else torch.empty(s, dtype=self.act, device=self.device)
                  for n, s in shapes.items()}
             L.moe_glu_backward(self.h, C, x, counts, dy, g["dx"], g["dW13"], g["dW2"],
                                L.MOE_BWD_SKIP_EMPTY_EXPERTS if skip_empty_experts else 0, st)
-        return g
+            return g
+        return launch_on(self.device, stream, (x, counts, dy, *out.values()), call)
 
     def check(self, stream=None) -> None:
         """Synchronise and raise a pending device error of this handle."""
-        with on_stream(self.device, stream) as st:
-            L.moe_glu_check(self.h, st)
+        launch_on(self.device, stream, (), lambda st: L.moe_glu_check(self.h, st))
 
     def close(self) -> None:
         if getattr(self, "h", None):

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
-from .experts import check_tensor, on_stream
+from .experts import check_tensor, launch_on
 
 BLOCK = 128
 E4M3 = torch.float8_e4m3fn
@@ -41,11 +41,13 @@ def quantize_rows(x: torch.Tensor, out=None, stream=None):
     if out is not None:
         check_tensor("q", out[0], x.shape, E4M3, x.device)
         check_tensor("s", out[1], sshape, torch.float32, x.device)
-    with on_stream(x.device, stream, x, *(out or ())) as st:
+
+    def call(st):
         q, s = out if out is not None else (torch.empty(x.shape, dtype=E4M3, device=x.device),
                                             torch.empty(sshape, dtype=torch.float32, device=x.device))
         L.moe_fp8_quantize_rows(x.numel() // K if K else 0, K, x, q, s, st)
-    return q, s
+        return q, s
+    return launch_on(x.device, stream, (x, *(out or ())), call)
 
 
 def quantize_weights(W: torch.Tensor, stream=None):
@@ -55,11 +57,13 @@ def quantize_weights(W: torch.Tensor, stream=None):
     if W.dim() != 3:
         raise ValueError("W must be [E, K, N]")
     E, K, N = W.shape
-    with on_stream(W.device, stream, W) as st:
+
+    def call(st):
         q = torch.empty(E, N, K, dtype=E4M3, device=W.device)
         s = torch.empty(E, blocks(N), blocks(K), dtype=torch.float32, device=W.device)
         L.moe_fp8_quantize_weights(E, K, N, W, q, s, st)
-    return q, s
+        return q, s
+    return launch_on(W.device, stream, (W,), call)
 
 
 class Fp8Matmul:
@@ -87,15 +91,16 @@ class Fp8Matmul:
         check_tensor("counts", counts, (self.E,), torch.int32, self.device)
         if out is not None:
             check_tensor("out", out, (self.E, C, self.N), torch.bfloat16, self.device)
-        with on_stream(self.device, stream, xq, xs, counts, out) as st:
+
+        def call(st):
             y = torch.empty(self.E, C, self.N, dtype=torch.bfloat16, device=self.device) if out is None else out
             L.moe_fp8_matmul(self.h, C, xq, xs, counts, y, st)
-        return y
+            return y
+        return launch_on(self.device, stream, (xq, xs, counts, out), call)
 
     def check(self, stream=None) -> None:
         """Synchronise and raise a pending device error of this handle."""
-        with on_stream(self.device, stream) as st:
-            L.moe_fp8_check(self.h, st)
+        launch_on(self.device, stream, (), lambda st: L.moe_fp8_check(self.h, st))
 
     def close(self) -> None:
         if getattr(self, "h", None):
