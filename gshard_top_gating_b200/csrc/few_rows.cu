@@ -2,20 +2,22 @@
 // few rows, or when 256 x 256 tiles would leave most of the device idle: the weights are what
 // has to be read, so they stream through every SM, and the rows ride along.
 //
-// The product is transposed: a tile is 128 columns of the result (features) times NT rows,
-// with the weights as the MMA's 128-row operand and the rows as its NT-column operand, so the
+// The product is transposed: a tile is 128 or 256 columns of the result (features; `up`: 128 of
+// g and the same of u) times NT rows, with the weights as the MMA's 128-row operand and the rows as its NT-column operand, so the
 // tensor cores' work follows the number of rows (16 at least) instead of 128-row tiles.
 //
 // Work is cut along the depth.  All tiles of all experts form one line of tiles x KB blocks
-// (a block: 64 deep in bf16, 128 in e4m3), of which every CTA takes an equal, contiguous
-// share, whatever the counts are: an expert without rows has no tiles, and two busy experts
-// of 256 keep all SMs at work.  A CTA's share may end inside a tile.  It then writes its
-// partial sum (fp32) to the workspace, and the last of the tile's CTAs to arrive adds all
-// parts in the order of the depth, so that results do not depend on timing, and finishes the
+// (a block: 64 deep in bf16, 128 in e4m3): an expert without rows has no tiles, and two busy
+// experts of 256 keep all SMs at work.  Most of the line is dealt out beforehand, an equal,
+// contiguous share to every CTA; where shares are long (kLongShare blocks), its last fifth is
+// cut into pieces that CTAs fetch as they finish, since SMs do not get the same share of the
+// memory's bandwidth.  The cuts depend on the counts alone.  A CTA that holds part of a tile
+// writes its sum (fp32) to the workspace, and the last of the tile's parts to arrive adds all
+// of them in the order of the depth -- so results do not depend on timing -- and finishes the
 // tile.  Nobody waits for another CTA.
 //
-// What bounds it: the bytes of the weights.  32 KB (16 KB) of weights per stage and up to
-// 12 stages keep about 200 KB per SM in flight.  Warp 0 loads (TMA), warp 1 issues MMAs and
+// What bounds it: the bytes of the weights.  Stages of 32 KB of weights keep about 200 KB per
+// SM in flight (16 KB stages lost 10-15% to the hand-over of a stage).  Warp 0 loads (TMA), warp 1 issues MMAs and
 // owns TMEM, warps 2..5 take the accumulator out.  For 8-bit weights they do so after every
 // block, since its scales differ: acc += (xs ws) * block, as in fp8.cu.  `down` starts its
 // weight loads while `up` drains; only the loads of h wait for it.  Every wait is bounded.
@@ -32,58 +34,90 @@ constexpr int kThreads = 192;
 constexpr uint32_t A_BYTES = 16384;         // 128 features x 128 bytes of depth
 enum { kUp = 0, kDown = 1, kFp8 = 2 };
 constexpr int kMinShare = 4;                // blocks per CTA, at least
+constexpr int kLongShare = 32;              // blocks per CTA from which the last fifth is fetched
+constexpr int kPieces = 4;                  // pieces per CTA in it, at most
+constexpr uint32_t kPieceBytes = 256 * 1024;   // weights of a piece, at least (about 6 us of an SM's bandwidth)
+constexpr int kRing = 4;                    // fetched pieces known ahead
 
 template <int KIND, int NT>
 struct Few {
-  static constexpr int ACC = KIND == kUp ? 2 : 1;               // accumulators (g and u)
+  // accumulators: g and u of 128 features, or two times 128 features (64 rows of an 8-bit
+  // product: one, its sums are kept in registers)
+  static constexpr int ACC = KIND == kFp8 && NT > 32 ? 1 : 2;
+  static constexpr int FEATURES = KIND == kUp ? 128 : 128 * ACC;   // of a tile
   static constexpr uint32_t STAGE = ACC * A_BYTES + NT * 128;
   static constexpr int FIT = (int)((220 * 1024) / STAGE);
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
   static constexpr int BUFS = KIND == kFp8 ? 4 : 2;             // accumulator buffers in TMEM
   static constexpr int COLS = BUFS * ACC * NT;
   static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr bool FETCH = NT <= 32;                       // (wider tiles: the parts would take too much memory)
   static constexpr uint32_t kBars = 512;
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kBars + 16 + 4 * (3 * kMaxExperts + 1);
+  static constexpr uint32_t kMisc = 128;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kBars + kMisc + 4 * (3 * kMaxExperts + 1);
   static_assert(COLS <= 512, "TMEM columns");
-  static_assert(8 * (2 * STAGES + 2 * BUFS + 1) <= (int)kBars, "barriers");
+  static_assert(8 * (2 * STAGES + 2 * BUFS + 1 + 2 * kRing) <= (int)kBars, "barriers");
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
   static_assert(SMEM + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
 };
 
 struct FewArgs {
   const int32_t* n;      // [E] rows per expert, clamped to [0, C]
-  int E, C, N, KB, NTn;  // features, blocks of depth, tiles of 128 features
+  int E, C, N, KB, NB;   // features, blocks of depth, blocks of 128 features
   int64_t Cb, Cd;        // rows per expert of the rows' operand and of the output
   int K;                 // rows of a bf16 weight matrix (its depth)
   __nv_bfloat16* D;      // output, N columns
   __nv_bfloat16* gu;     // kUp: [g|u], 2N columns, or null
   const float* xs;       // kFp8: [E, C, KB]
-  const float* ws;       // kFp8: [E, NTn, KB]
-  float* part;           // [2 * grid][ACC * NT][128] partial sums
-  unsigned* count;       // [grid] parts of a tile that have arrived; zero between launches
+  const float* ws;       // kFp8: [E, NB, KB]
+  float* part;           // [(2 + kPieces) * grid][ACC * NT][128] partial sums
+  unsigned* count;       // arrivals: [grid] tiles of shares, [kPieces * grid] fetched tiles; then
+                         // the next piece, and CTAs that found none.  Zero between launches
   unsigned* err;
   uint64_t limit_ns;
 };
 
-// The line of blocks and this CTA's share of it.
-struct Share {
-  long long U;           // blocks in all
+// How the line is cut, and where this CTA's share of it begins (one copy per CTA).
+struct Cuts {
+  int T, Ts;             // tiles in all, and those dealt out as shares
   int G;                 // CTAs that have a share
-  __device__ long long first(int i) const { return U * i / G; }
-  // the CTA whose share holds block u: the largest i with U i / G <= u
-  __device__ int owner(long long u) const { return (int)(((u + 1) * G - 1) / U); }
+  int P;                 // pieces of each of the other tiles
+  int t0, kb0, len;      // this CTA's share: tile, block, blocks
+  int pad;
 };
+
+// floor(i * U / G) and the CTA whose share holds block u: the largest i with U i / G <= u
+__device__ __forceinline__ long long share_first(long long U, int G, int i) {
+  return U * i <= 0xFFFFFFFFll ? (long long)((uint32_t)(U * i) / (uint32_t)G) : U * i / G;
+}
+__device__ __forceinline__ int share_owner(long long U, int G, long long u) {
+  const long long a = (u + 1) * G - 1;
+  return (a | U) <= 0xFFFFFFFFll ? (int)((uint32_t)a / (uint32_t)U) : (int)(a / U);
+}
 
 // Tiles in the order (expert, features, rows), rows fastest: a weight tile is read by
 // neighbours in the line.
 struct Tile {
   int e, nt, rt;
 };
-__device__ __forceinline__ Tile tile_at(int t, const int* pre, const int* rtiles, int& e) {
-  while (t >= pre[e + 1]) ++e;
-  const int local = t - pre[e];
-  return Tile{e, local / rtiles[e], local % rtiles[e]};
+__device__ __forceinline__ Tile tile_at(int t, const int* pre, const int* rtiles, int E) {
+  int lo = 0, hi = E;        // pre[lo] <= t < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int local = t - pre[lo], r = rtiles[lo];
+  const int nt = r == 1 ? local : local / r;
+  return Tile{lo, nt, local - nt * r};
 }
+
+// The walk of one role over the CTA's work: its share, tile by tile, then fetched pieces,
+// whose numbers the producer passes on through a ring.
+struct Step {
+  int t, kb, len;        // tile, first block, blocks
+  int piece;             // fetched: its number, else -1
+};
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -107,19 +141,21 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
 // The four epilogue warps meet.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// One finished element: feature f of row c of the tile (c may lie past the expert's rows only
-// where zeros are wanted).
-template <int KIND, int FN>
-__device__ __forceinline__ void put(const FewArgs& a, int64_t row, int f, float v0, float v1, bool live) {
+// Finished values of one row: feature f (and f + 128) of a tile.  `live` false: zeros.
+template <int KIND, int ACC, int FN>
+__device__ __forceinline__ void put(const FewArgs& a, int64_t row, int f, const float (&v)[ACC], bool live) {
   if (KIND == kUp) {
-    const float h = glu_f<FN, true>(v0) * v1;
+    if (f >= a.N) return;
+    const float h = glu_f<FN, true>(v[0]) * v[1];
     a.D[row * a.N + f] = __float2bfloat16_rn(live ? h : 0.f);
     if (a.gu) {
-      a.gu[row * 2 * a.N + f] = __float2bfloat16_rn(live ? v0 : 0.f);
-      a.gu[row * 2 * a.N + a.N + f] = __float2bfloat16_rn(live ? v1 : 0.f);
+      a.gu[row * 2 * a.N + f] = __float2bfloat16_rn(live ? v[0] : 0.f);
+      a.gu[row * 2 * a.N + a.N + f] = __float2bfloat16_rn(live ? v[1] : 0.f);
     }
   } else {
-    a.D[row * a.N + f] = __float2bfloat16_rn(v0);
+#pragma unroll
+    for (int j = 0; j < ACC; ++j)
+      if (f + j * 128 < a.N) a.D[row * a.N + f + j * 128] = __float2bfloat16_rn(v[j]);
   }
 }
 
@@ -138,15 +174,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + BUFS + b); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 2 * BUFS);
+  auto pfull_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + r); };
+  auto pempty_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + kRing + r); };
   unsigned char* misc = gbase + STAGES * F::STAGE + F::kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile unsigned* arrived = reinterpret_cast<volatile unsigned*>(misc + 8);
-  int* pre = reinterpret_cast<int*>(misc + 16);        // [E + 1] first tile of each expert
+  volatile int* ring = reinterpret_cast<volatile int*>(misc + 16);
+  Cuts* cuts = reinterpret_cast<Cuts*>(misc + 32);
+  int* pre = reinterpret_cast<int*>(misc + F::kMisc);  // [E + 1] first tile of each expert
   int* rtiles = pre + (kMaxExperts + 1);               // [E] tiles of NT rows
   int* nrows = rtiles + kMaxExperts;                   // [E]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = a.KB, grid = (int)gridDim.x, me = (int)blockIdx.x;
+  const int NTn = (a.N + F::FEATURES - 1) / F::FEATURES;
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -157,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(b), 4);
     }
     mbar_init(done_bar, 1);
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(pfull_bar(r), 1);
+      mbar_init(pempty_bar(r), 5);             // the MMA thread and four epilogue warps
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&tmW);
@@ -179,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = e0; e < min(a.E, e0 + per); ++e) {
       nrows[e] = min(max(a.n[e], 0), a.C);
       rtiles[e] = (nrows[e] + NT - 1) / NT;
-      sum += rtiles[e] * a.NTn;
+      sum += rtiles[e] * NTn;
     }
     int inc = sum;
 #pragma unroll
@@ -190,69 +236,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     int run = inc - sum;
     for (int e = e0; e < min(a.E, e0 + per); ++e) {
       pre[e] = run;
-      run += rtiles[e] * a.NTn;
+      run += rtiles[e] * NTn;
     }
-    if (lane == 31) pre[a.E] = inc;
+    if (lane == 31) {
+      pre[a.E] = inc;
+      Cuts c{};
+      c.T = c.Ts = inc;
+      c.P = 1;
+      if (F::FETCH && (long long)inc * KB >= (long long)kLongShare * grid) {
+        const int td = min(inc / 5, kPieces * grid);
+        if (td > 0) {
+          c.Ts = inc - td;
+          c.P = max(1, min((int)(KB * (ACC * A_BYTES) / kPieceBytes), kPieces * grid / td));
+        }
+      }
+      const long long U = (long long)c.Ts * KB;
+      c.G = (int)min((long long)grid, (U + kMinShare - 1) / kMinShare);
+      if (me < c.G) {
+        const long long u0 = share_first(U, c.G, me), u1 = share_first(U, c.G, me + 1);
+        c.t0 = u0 <= 0xFFFFFFFFll ? (int)((uint32_t)u0 / (uint32_t)KB) : (int)(u0 / KB);
+        c.kb0 = (int)(u0 - (long long)c.t0 * KB);
+        c.len = (int)(u1 - u0);
+      }
+      *cuts = c;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int KB = a.KB;
-  Share sh;
-  sh.U = (long long)pre[a.E] * KB;
-  sh.G = (int)min((long long)gridDim.x, (sh.U + kMinShare - 1) / kMinShare);
-  const int me = blockIdx.x;
-  const bool mine = me < sh.G;
-  const long long u0 = mine ? sh.first(me) : 0, u1 = mine ? sh.first(me + 1) : 0;
+  const Cuts c = *cuts;
+  const int npieces = (c.T - c.Ts) * c.P;
+  auto piece = [&](int id) {                           // a fetched piece
+    const int i = id / c.P, p = id - i * c.P;
+    const int kb = KB * p / c.P;
+    return Step{c.Ts + i, kb, KB * (p + 1) / c.P - kb, id};
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int s = 0, e = 0;
+      int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
       bool ok = true;
       auto load_w = [&](int st, const Tile& t, int kb) {
         const uint32_t sa = base + st * F::STAGE;
         mbar_arrive_expect_tx(full_bar(st), F::STAGE);
+        // features past N read the next rows or columns, or zeros; they are not stored
         if (KIND == kFp8) {
-          tma_load_2d(sa, &tmW, full_bar(st), kb * 128, t.e * a.N + t.nt * 128);
+          tma_load_2d(sa, &tmW, full_bar(st), kb * 128, t.e * a.N + t.nt * F::FEATURES);
+        } else if (KIND == kDown) {
+          tma_load_3d(sa, &tmW, full_bar(st), 0, t.e * a.K + kb * 64, t.nt * 4);
         } else {
-          // features past N read the next columns or zeros; they are not stored
-#pragma unroll
-          for (int c = 0; c < ACC; ++c)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              tma_load_2d(sa + c * A_BYTES + j * 8192u, &tmW, full_bar(st), c * a.N + t.nt * 128 + j * 64, t.e * a.K + kb * 64);
+          tma_load_3d(sa, &tmW, full_bar(st), 0, t.e * a.K + kb * 64, t.nt * 2);
+          tma_load_3d(sa + A_BYTES, &tmW, full_bar(st), 0, t.e * a.K + kb * 64, a.N / 64 + t.nt * 2);
         }
       };
       auto load_x = [&](int st, const Tile& t, int kb) {
         tma_load_2d(base + st * F::STAGE + ACC * A_BYTES, &tmX, full_bar(st), kb * (KIND == kFp8 ? 128 : 64),
                     (int)(t.e * a.Cb) + t.rt * NT);
       };
-      long long u = u0;
-      if (KIND == kDown) {
-        // the first stages' weights before `up` has finished, then the rows it wrote
-        const int lead = (int)min((long long)STAGES, u1 - u0);
-        int e2 = 0;
-        for (int i = 0; i < lead; ++i) load_w(i, tile_at((int)((u0 + i) / KB), pre, rtiles, e2), (int)((u0 + i) % KB));
-        pdl_wait();
-        for (int i = 0; i < lead; ++i) load_x(i, tile_at((int)((u0 + i) / KB), pre, rtiles, e), (int)((u0 + i) % KB));
-        issued = (1u << lead) - 1u;
-        u += lead;
-        s = lead % STAGES;
-        ph = lead == STAGES ? 1u : 0u;
-      }
-      while (ok && u < u1) {
-        const Tile t = tile_at((int)(u / KB), pre, rtiles, e);
-        int kb = (int)(u % KB);
-        const int end = (int)min((long long)KB, kb + (u1 - u));
-        u += end - kb;
-        for (; kb < end; ++kb) {
+      auto load = [&](const Step& st) {
+        const Tile t = tile_at(st.t, pre, rtiles, a.E);
+        for (int kb = st.kb; kb < st.kb + st.len; ++kb) {
           if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
-            break;
+            return;
           }
           load_w(s, t, kb);
           load_x(s, t, kb);
@@ -262,6 +312,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             s = 0;
             ph ^= 1u;
           }
+        }
+      };
+      int t = c.t0, kb = c.kb0, left = c.len;
+      if (KIND == kDown) {
+        // the first stages' weights before `up` has finished, then the rows it wrote
+        const int lead = min(STAGES, left);
+        for (int pass = 0; pass < 2; ++pass) {
+          t = c.t0;
+          kb = c.kb0;
+          Tile tile = lead ? tile_at(t, pre, rtiles, a.E) : Tile{0, 0, 0};
+          for (int i = 0; i < lead; ++i) {
+            if (pass == 0) load_w(i, tile, kb);
+            else load_x(i, tile, kb);
+            if (++kb == KB) {
+              kb = 0;
+              if (++t < c.T) tile = tile_at(t, pre, rtiles, a.E);
+            }
+          }
+          if (pass == 0) pdl_wait();
+        }
+        issued = (1u << lead) - 1u;
+        left -= lead;
+        s = lead % STAGES;
+        ph = lead == STAGES ? 1u : 0u;
+      }
+      while (ok && left > 0) {
+        const Step st{t, kb, min(KB - kb, left), -1};
+        load(st);
+        left -= st.len;
+        ++t;
+        kb = 0;
+      }
+      if (F::FETCH && npieces > 0) {
+        unsigned* next = a.count + (1 + kPieces) * grid;
+        int id = ok ? (int)atomicAdd(next, 1u) : npieces;
+        for (int r = 0;; ++r) {
+          const int slot = r % kRing;
+          if (!ok || *abort_flag || !mbar_wait(pempty_bar(slot), ((r / kRing) & 1) ^ 1, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          ring[slot] = id;
+          mbar_arrive(pfull_bar(slot));
+          if (id >= npieces) break;
+          const int then = (int)atomicAdd(next, 1u);
+          load(piece(id));
+          id = then;
+        }
+        if (ok && atomicAdd(next + 1, 1u) == (unsigned)grid - 1u) {   // every CTA has found none left
+          next[0] = 0u;
+          next[1] = 0u;
         }
       }
       if (!ok) {   // let copies in flight land before the CTA exits
@@ -273,26 +375,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      int s = 0, buf = 0, e = 0;
+      int s = 0, buf = 0;
       uint32_t ph = 0, bph = 0;
       bool ok = true;
-      for (long long u = u0; ok && u < u1;) {
-        const Tile t = tile_at((int)(u / KB), pre, rtiles, e);
-        const int kb0 = (int)(u % KB);
-        const int len = (int)min((long long)(KB - kb0), u1 - u);
-        u += len;
+      auto mma = [&](const Step& st) {
+        const Tile t = tile_at(st.t, pre, rtiles, a.E);
         // rows of this tile, rounded up to the MMA's step of 16 columns
         const int cols = (min(NT, nrows[t.e] - t.rt * NT) + 15) & ~15;
         // D fp32, M = 128, N = cols; bf16: A with its rows (features) contiguous, B its depth
         const uint32_t idesc = (1u << 4) | (KIND == kFp8 ? 0u : (1u << 7) | (1u << 10) | (1u << 15)) |
                                ((uint32_t)(cols >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-        for (int i = 0; i < len; ++i) {
+        for (int i = 0; i < st.len; ++i) {
           const bool fresh = KIND == kFp8 || i == 0;
           if (*abort_flag || (fresh && !mbar_wait(tempty_bar(buf), bph ^ 1u, a.err, a.limit_ns)) ||
               !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
-            break;
+            return;
           }
           tc_fence_after();
           const uint32_t sa = base + s * F::STAGE, sb = sa + ACC * A_BYTES;
@@ -300,16 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t bd = desc_sw128(sb + kk * 32u, 16u, 1024u);
-            if (KIND == kFp8) {
-              tc_mma_f8(d, desc_sw128(sa + kk * 32u, 16u, 1024u), bd, idesc, kk != 0);
-            } else {
 #pragma unroll
-              for (int c = 0; c < ACC; ++c)
-                tc_mma_f16(d + c * NT, desc_sw128(sa + c * A_BYTES + kk * 2048u, 8192u, 1024u), bd, idesc, (i | kk) != 0);
+            for (int j = 0; j < ACC; ++j) {
+              if (KIND == kFp8)
+                tc_mma_f8(d + j * NT, desc_sw128(sa + j * A_BYTES + kk * 32u, 16u, 1024u), bd, idesc, kk != 0);
+              else
+                tc_mma_f16(d + j * NT, desc_sw128(sa + j * A_BYTES + kk * 2048u, 8192u, 1024u), bd, idesc, (i | kk) != 0);
             }
           }
           tc_commit(empty_bar(s));
-          if (KIND == kFp8 || i == len - 1) {
+          if (KIND == kFp8 || i == st.len - 1) {
             tc_commit(tfull_bar(buf));
             if (++buf == BUFS) {
               buf = 0;
@@ -321,7 +420,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
         }
+      };
+      int t = c.t0, kb = c.kb0, left = c.len;
+      while (ok && left > 0) {
+        const Step st{t, kb, min(KB - kb, left), -1};
+        mma(st);
+        left -= st.len;
+        ++t;
+        kb = 0;
       }
+      if (F::FETCH && npieces > 0)
+        for (int r = 0; ok; ++r) {
+          const int slot = r % kRing;
+          if (*abort_flag || !mbar_wait(pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const int id = ring[slot];
+          mbar_arrive(pempty_bar(slot));
+          if (id >= npieces) break;
+          mma(piece(id));
+        }
       if (!ok) {   // let issued MMAs finish before TMEM is released
         tc_commit(done_bar);
         mbar_wait(done_bar, 0, a.err, a.limit_ns);
@@ -333,54 +453,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;                    // TMEM lane quarter of this warp
     const int lane128 = q * 32 + lane;         // this thread's feature within a tile
     if (KIND == kDown) pdl_wait();             // the workspace is `up`'s until it has finished
-    int buf = 0, e = 0;
+    int buf = 0;
     uint32_t bph = 0;
     bool ok = true;
-    for (long long u = u0; ok && u < u1;) {
-      const int ti = (int)(u / KB);
-      const Tile t = tile_at(ti, pre, rtiles, e);
-      const int kb0 = (int)(u % KB);
-      const int len = (int)min((long long)(KB - kb0), u1 - u);
-      u += len;
+    auto take = [&](const Step& st) {
+      const Tile t = tile_at(st.t, pre, rtiles, a.E);
       const int row0 = t.rt * NT, left = nrows[t.e] - row0;
       const int nvalid = min(NT, left);
-      const bool whole = len == KB;
-      const int f = t.nt * 128 + lane128;
+      const bool whole = st.len == KB;
+      const int f = t.nt * F::FEATURES + lane128;
       const int64_t drow = t.e * a.Cd + row0;
       // training: the rows up to the next multiple of 64 are zeros (weight gradients reduce
       // over whole blocks of 64)
       const int nzero = KIND == kUp && a.gu && left <= NT ? (nrows[t.e] + 63) / 64 * 64 - row0 : 0;
-      float* part = a.part + (size_t)(2 * me + (kb0 == 0)) * ACC * NT * 128 + lane128;
+      const int slot = st.piece >= 0 ? 2 * grid + st.piece : 2 * me + (st.kb == 0);
+      float* part = a.part + (size_t)slot * (ACC * NT * 128) + lane128;
       const uint32_t tm0 = tmem_base + ((uint32_t)(q * 32) << 16);
       if constexpr (KIND == kFp8) {
-        float sum[NT];
+        float sum[ACC][NT];
 #pragma unroll
-        for (int c = 0; c < NT; ++c) sum[c] = 0.f;
-        const float* ws = a.ws + ((int64_t)t.e * a.NTn + t.nt) * KB;
+        for (int j = 0; j < ACC; ++j)
+#pragma unroll
+          for (int k = 0; k < NT; ++k) sum[j][k] = 0.f;
+        const float* ws = a.ws + ((int64_t)t.e * a.NB + t.nt * ACC) * KB;
+        const bool second = ACC == 2 && t.nt * ACC + 1 < a.NB;      // the tile has a second block of 128
         const float* xs = a.xs + (t.e * a.Cb + row0) * KB;
         constexpr int XR = (NT + 31) / 32;     // lane l holds the scales of rows l, l + 32, ...
-        float x[2][XR], w[2];
-        auto scales = [&](int i, float (&xv)[XR], float& wv) {
-          const int kb = kb0 + i;
-          wv = i < len ? __ldg(ws + kb) : 0.f;
+        constexpr int AHEAD = 4;               // blocks whose scales are on their way
+        float x[AHEAD][XR], w[AHEAD][ACC];
+        auto scales = [&](int i, float (&xv)[XR], float (&wv)[ACC]) {
+          const int kb = st.kb + i;
+          wv[0] = i < st.len ? __ldg(ws + kb) : 0.f;
+          if (ACC == 2) wv[ACC - 1] = i < st.len && second ? __ldg(ws + KB + kb) : 0.f;
 #pragma unroll
           for (int r = 0; r < XR; ++r)
-            xv[r] = i < len && r * 32 + lane < nvalid ? __ldg(xs + (int64_t)(r * 32 + lane) * KB + kb) : 0.f;
+            xv[r] = i < st.len && r * 32 + lane < nvalid ? __ldg(xs + (int64_t)(r * 32 + lane) * KB + kb) : 0.f;
         };
-        auto drain = [&](int i, float (&xv)[XR], float& wv) -> bool {
+        auto drain = [&](int i, float (&xv)[XR], float (&wv)[ACC]) {
           if (*abort_flag || !mbar_wait(tfull_bar(buf), bph, a.err, a.limit_ns)) {
             *abort_flag = 1;
-            return false;
+            ok = false;
+            return;
           }
           tc_fence_after();
-          float sc[XR];
+          float sx[XR], sw[ACC];
 #pragma unroll
-          for (int r = 0; r < XR; ++r) sc[r] = xv[r] * wv;
-          scales(i + 2, xv, wv);
-          uint32_t v[NT / 16][16];
+          for (int r = 0; r < XR; ++r) sx[r] = xv[r];
 #pragma unroll
-          for (int c = 0; c < NT / 16; ++c)
-            if (c * 16 < nvalid) tmem_ld_32x32b_x16(tm0 + buf * NT + c * 16, v[c]);
+          for (int j = 0; j < ACC; ++j) sw[j] = wv[j];
+          scales(i + AHEAD, xv, wv);
+          uint32_t v[ACC][NT / 16][16];
+#pragma unroll
+          for (int k = 0; k < NT / 16; ++k)
+            if (k * 16 < nvalid) {
+#pragma unroll
+              for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm0 + buf * (ACC * NT) + j * NT + k * 16, v[j][k]);
+            }
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -390,33 +518,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             bph ^= 1u;
           }
 #pragma unroll
-          for (int c = 0; c < NT / 16; ++c)
-            if (c * 16 < nvalid) {
+          for (int k = 0; k < NT / 16; ++k)
+            if (k * 16 < nvalid) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int col = c * 16 + j;
-                sum[col] = fmaf(__shfl_sync(0xffffffffu, sc[col / 32], col % 32), __uint_as_float(v[c][j]), sum[col]);
+              for (int i2 = 0; i2 < 16; ++i2) {
+                const int col = k * 16 + i2;
+                const float s = __shfl_sync(0xffffffffu, sx[col / 32], col % 32);
+#pragma unroll
+                for (int j = 0; j < ACC; ++j)
+                  sum[j][col] = fmaf(s * sw[j], __uint_as_float(v[j][k][i2]), sum[j][col]);
               }
             }
-          return true;
         };
-        scales(0, x[0], w[0]);
-        scales(1, x[1], w[1]);
-        for (int i = 0; ok && i < len; i += 2) {
-          ok = drain(i, x[0], w[0]);
-          if (ok && i + 1 < len) ok = drain(i + 1, x[1], w[1]);
-        }
-        if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
-          if (c < nvalid) {
-            if (!whole) __stcg(part + c * 128, sum[c]);
-            else if (f < a.N) put<KIND, FN>(a, drow + c, f, sum[c], 0.f, true);
+        for (int d = 0; d < AHEAD; ++d) scales(d, x[d], w[d]);
+        for (int i = 0; ok && i < st.len; i += AHEAD)
+#pragma unroll
+          for (int d = 0; d < AHEAD; ++d)
+            if (ok && i + d < st.len) drain(i + d, x[d], w[d]);
+        if (!ok) return;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+          if (k < nvalid) {
+            float v[ACC];
+#pragma unroll
+            for (int j = 0; j < ACC; ++j) v[j] = sum[j][k];
+            if (whole) {
+              put<KIND, ACC, FN>(a, drow + k, f, v, true);
+            } else {
+#pragma unroll
+              for (int j = 0; j < ACC; ++j) __stcg(part + (j * NT + k) * 128, v[j]);
+            }
           }
       } else {
         if (*abort_flag || !mbar_wait(tfull_bar(buf), bph, a.err, a.limit_ns)) {
           *abort_flag = 1;
-          break;
+          ok = false;
+          return;
         }
         tc_fence_after();
         const uint32_t tm = tm0 + buf * (ACC * NT);
@@ -424,16 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = 0; c0 < nvalid; c0 += 16) {
           uint32_t v[ACC][16];
 #pragma unroll
-          for (int c = 0; c < ACC; ++c) tmem_ld_32x32b_x16(tm + c * NT + c0, v[c]);
+          for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm + j * NT + c0, v[j]);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c0 + j >= nvalid) break;
-            if (!whole) {
+          for (int i = 0; i < 16; ++i) {
+            if (c0 + i >= nvalid) break;
+            float s[ACC];
 #pragma unroll
-              for (int c = 0; c < ACC; ++c) __stcg(part + (c * NT + c0 + j) * 128, __uint_as_float(v[c][j]));
-            } else if (f < a.N) {
-              put<KIND, FN>(a, drow + c0 + j, f, __uint_as_float(v[0][j]), __uint_as_float(v[ACC - 1][j]), true);
+            for (int j = 0; j < ACC; ++j) s[j] = __uint_as_float(v[j][i]);
+            if (whole) {
+              put<KIND, ACC, FN>(a, drow + c0 + i, f, s, true);
+            } else {
+#pragma unroll
+              for (int j = 0; j < ACC; ++j) __stcg(part + (j * NT + c0 + i) * 128, s[j]);
             }
           }
         }
@@ -447,40 +588,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool finish = whole;
       if (!whole) {
-        // a part of a tile: the last CTA to bring one adds them all, in the order of the depth
-        const long long first = (long long)ti * KB;
-        const int i0 = sh.owner(first), i1 = sh.owner(first + KB - 1);
-        __threadfence();
+        // a part of a tile: the last one to come adds them all, in the order of the depth
+        int first, parts, counter;
+        if (st.piece >= 0) {
+          const int i = st.t - c.Ts;
+          first = 2 * grid + i * c.P;
+          parts = c.P;
+          counter = grid + i;
+        } else {
+          const long long U = (long long)c.Ts * KB, u = (long long)st.t * KB;
+          const int i0 = share_owner(U, c.G, u);
+          parts = share_owner(U, c.G, u + KB - 1) - i0 + 1;
+          first = 2 * i0 + 1;                  // the tile's first CTA, then slot 0 of the next ones
+          counter = i0;
+        }
         epi_sync();
-        if (threadIdx.x == 64) *arrived = atomicAdd(a.count + i0, 1u);
-        epi_sync();
-        finish = *arrived == (unsigned)(i1 - i0);
-        if (finish) {
+        if (threadIdx.x == 64) {
           __threadfence();
-          if (threadIdx.x == 64) a.count[i0] = 0u;
-          if (f < a.N) {
+          const unsigned before = atomicAdd(a.count + counter, 1u);
+          __threadfence();
+          if (before == (unsigned)parts - 1u) a.count[counter] = 0u;
+          *arrived = before;
+        }
+        epi_sync();
+        finish = *arrived == (unsigned)parts - 1u;
+        if (finish) {
+          const float* p0 = a.part + (size_t)first * (ACC * NT * 128) + lane128;
+          // from one part's slot to the next: 1 for pieces; for shares 2 i0 + 1, 2 i0 + 2, 2 i0 + 4, ...
+          auto at = [&](int i) {
+            const int d = st.piece >= 0 ? i : i == 0 ? 0 : 2 * i - 1;
+            return p0 + (size_t)d * (ACC * NT * 128);
+          };
 #pragma unroll 1
-            for (int c0 = 0; c0 < nvalid; c0 += 8) {
-              float s[ACC][8] = {};
-#pragma unroll 2
-              for (int i = i0; i <= i1; ++i) {
-                const float* p = a.part + (size_t)(2 * i + (i == i0)) * ACC * NT * 128 + lane128;
+          for (int c0 = 0; c0 < nvalid; c0 += 8) {
+            float s[ACC][8] = {};
+#pragma unroll 1
+            for (int i = 0; i < parts; i += 4) {         // four parts' loads in flight
+              float v[4][ACC][8];
 #pragma unroll
-                for (int c = 0; c < ACC; ++c)
+              for (int d = 0; d < 4; ++d) {
+                const float* p = at(i + d);
 #pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    if (c0 + j < nvalid) s[c][j] += __ldcg(p + (c * NT + c0 + j) * 128);
+                for (int j = 0; j < ACC; ++j)
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    v[d][j][k] = i + d < parts && c0 + k < nvalid ? __ldcg(p + (j * NT + c0 + k) * 128) : 0.f;
               }
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (c0 + j < nvalid) put<KIND, FN>(a, drow + c0 + j, f, s[0][j], s[ACC - 1][j], true);
+              for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int j = 0; j < ACC; ++j)
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) s[j][k] += v[d][j][k];
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (c0 + k < nvalid) {
+                float v[ACC];
+#pragma unroll
+                for (int j = 0; j < ACC; ++j) v[j] = s[j][k];
+                put<KIND, ACC, FN>(a, drow + c0 + k, f, v, true);
+              }
           }
         }
       }
-      if (KIND == kUp && finish && f < a.N)
-        for (int c = nvalid; c < nzero; ++c) put<KIND, FN>(a, drow + c, f, 0.f, 0.f, false);
+      if (KIND == kUp && finish) {
+        const float zero[ACC] = {};
+        for (int k = nvalid; k < nzero; ++k) put<KIND, ACC, FN>(a, drow + k, f, zero, false);
+      }
+    };
+    int t = c.t0, kb = c.kb0, left = c.len;
+    while (ok && left > 0) {
+      const Step st{t, kb, min(KB - kb, left), -1};
+      take(st);
+      left -= st.len;
+      ++t;
+      kb = 0;
     }
+    if (F::FETCH && npieces > 0)
+      for (int r = 0; ok; ++r) {
+        const int slot = r % kRing;
+        if (*abort_flag || !mbar_wait(pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
+          *abort_flag = 1;
+          break;
+        }
+        const int id = ring[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pempty_bar(slot));
+        if (id >= npieces) break;
+        take(piece(id));
+      }
   }
 
   tc_fence_before();
@@ -524,14 +721,17 @@ constexpr int kMostBf16 = 128, kMostFp8 = 64;
 
 size_t few_rows_workspace(int64_t C_max, bool fp8, int num_sms, size_t* counts) {
   const int nt = row_tile(C_max, fp8 ? kMostFp8 : kMostBf16);
-  *counts = (size_t)num_sms;
-  return (size_t)2 * num_sms * (fp8 ? 1 : 2) * nt * 128;
+  *counts = (size_t)(1 + kPieces) * num_sms + 2;
+  // the widest tile takes most, the fetched pieces of tiles of up to 32 rows included
+  const size_t lane = (size_t)num_sms * 2 * 128;
+  const size_t shares = 2 * lane * nt, pieces = (2 + kPieces) * lane * (nt < 32 ? nt : 32);
+  return shares > pieces ? shares : pieces;
 }
 
 cudaError_t glu_few_up(const GluArgs& a) {
   const int nt = row_tile(a.C, kMostBf16);
   CUtensorMap tmW, tmX;
-  if (!encode_2d(&tmW, a.W13, 2 * (uint64_t)a.H, (uint64_t)a.E * a.M, 64, 64) ||
+  if (!encode_column_blocks(&tmW, a.W13, 2 * (uint64_t)a.H, (uint64_t)a.E * a.M, 2) ||
       !encode_2d(&tmX, a.x, a.M, (uint64_t)a.E * a.C, 64, nt))
     return cudaErrorInvalidValue;
   FewArgs f{};
@@ -541,7 +741,6 @@ cudaError_t glu_few_up(const GluArgs& a) {
   f.N = a.H;
   f.K = a.M;
   f.KB = a.M / 64;
-  f.NTn = (a.H + 127) / 128;
   f.Cb = a.C;
   f.Cd = a.Cp;
   f.D = static_cast<__nv_bfloat16*>(a.h);
@@ -558,7 +757,7 @@ cudaError_t glu_few_up(const GluArgs& a) {
 cudaError_t glu_few_down(const GluArgs& a) {
   const int nt = row_tile(a.C, kMostBf16);
   CUtensorMap tmW, tmX;
-  if (!encode_2d(&tmW, a.W2, a.M, (uint64_t)a.E * a.H, 64, 64) ||
+  if (!encode_column_blocks(&tmW, a.W2, a.M, (uint64_t)a.E * a.H, 4) ||
       !encode_2d(&tmX, a.h, a.H, (uint64_t)a.E * a.Cp, 64, nt))
     return cudaErrorInvalidValue;
   FewArgs f{};
@@ -568,7 +767,6 @@ cudaError_t glu_few_down(const GluArgs& a) {
   f.N = a.M;
   f.K = a.H;
   f.KB = a.H / 64;
-  f.NTn = (a.M + 127) / 128;
   f.Cb = a.Cp;
   f.Cd = a.C;
   f.D = static_cast<__nv_bfloat16*>(a.y);
@@ -582,7 +780,7 @@ cudaError_t glu_few_down(const GluArgs& a) {
 cudaError_t fp8_few(const Fp8Args& a) {
   const int nt = row_tile(a.C, kMostFp8);
   CUtensorMap tmW, tmX;
-  if (!encode_2d_bytes(&tmW, a.wq, a.K, (uint64_t)a.E * a.N, 128, 128) ||
+  if (!encode_2d_bytes(&tmW, a.wq, a.K, (uint64_t)a.E * a.N, 128, nt <= 32 ? 256 : 128) ||
       !encode_2d_bytes(&tmX, a.xq, a.K, (uint64_t)a.E * a.C, 128, nt))
     return cudaErrorInvalidValue;
   FewArgs f{};
@@ -591,7 +789,7 @@ cudaError_t fp8_few(const Fp8Args& a) {
   f.C = (int)a.C;
   f.N = a.N;
   f.KB = (a.K + 127) / 128;
-  f.NTn = (a.N + 127) / 128;
+  f.NB = (a.N + 127) / 128;
   f.Cb = a.C;
   f.Cd = a.C;
   f.D = static_cast<__nv_bfloat16*>(a.y);

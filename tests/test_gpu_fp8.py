@@ -134,6 +134,7 @@ CASES = [
     (16, 64, 2048, 384, [64, 33, 0, 1] * 4),
     (1, 1, 4096, 1024, [1]),
     (2, 30, 1168, 264, [30, 19]),
+    (32, 9, 2048, 1544, [i % 10 for i in range(32)]),        # long shares: part of the work is fetched
 ]
 
 
