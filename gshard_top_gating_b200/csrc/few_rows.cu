@@ -18,7 +18,9 @@
 //
 // What bounds it: the bytes of the weights.  Stages of 32 KB of weights keep about 200 KB per
 // SM in flight (16 KB stages lost 10-15% to the hand-over of a stage).  Warp 0 loads (TMA), warp 1 issues MMAs and
-// owns TMEM, warps 2..5 take the accumulator out.  For 8-bit weights they do so after every
+// owns TMEM, warps 2..5 take the accumulator out, warps 6..9 join parts: the memory fence, the
+// arrival and the other parts' loads take several us beside a saturated memory, which the
+// accumulators of the next pieces must not wait for.  For 8-bit weights they do so after every
 // block, since its scales differ: acc += (xs ws) * block, as in fp8.cu.  `down` starts its
 // weight loads while `up` drains; only the loads of h wait for it.  Every wait is bounded.
 #include "common.cuh"
@@ -30,7 +32,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;               // loads, MMAs, four epilogue and four joining warps
 constexpr uint32_t A_BYTES = 16384;         // 128 features x 128 bytes of depth
 enum { kUp = 0, kDown = 1, kFp8 = 2 };
 constexpr int kMinShare = 4;                // blocks per CTA, at least
@@ -38,6 +40,7 @@ constexpr int kLongShare = 32;              // blocks per CTA from which the las
 constexpr int kPieces = 4;                  // pieces per CTA in it, at most
 constexpr uint32_t kPieceBytes = 256 * 1024;   // weights of a piece, at least (about 6 us of an SM's bandwidth)
 constexpr int kRing = 4;                    // fetched pieces known ahead
+constexpr int kJoin = 4;                    // parts on their way to the joining warps
 
 template <int KIND, int NT>
 struct Few {
@@ -53,10 +56,10 @@ struct Few {
   static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr bool FETCH = NT <= 32;                       // (wider tiles: the parts would take too much memory)
   static constexpr uint32_t kBars = 512;
-  static constexpr uint32_t kMisc = 128;
+  static constexpr uint32_t kMisc = 256;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kBars + kMisc + 4 * (3 * kMaxExperts + 1);
   static_assert(COLS <= 512, "TMEM columns");
-  static_assert(8 * (2 * STAGES + 2 * BUFS + 1 + 2 * kRing) <= (int)kBars, "barriers");
+  static_assert(8 * (2 * STAGES + 2 * BUFS + 1 + 2 * kRing + 2 * kJoin) <= (int)kBars, "barriers");
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
   static_assert(SMEM + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
 };
@@ -138,8 +141,8 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// The four epilogue warps meet.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four joining warps meet.
+__device__ __forceinline__ void join_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // Finished values of one row: feature f (and f + 128) of a tile.  `live` false: zeros.
 template <int KIND, int ACC, int FN>
@@ -159,6 +162,14 @@ __device__ __forceinline__ void put(const FewArgs& a, int64_t row, int f, const 
   }
 }
 
+// Training: the rows of h and [g|u] from an expert's last one to the next multiple of 64 are
+// zeros, since the weight gradients reduce over whole blocks of 64.
+template <int KIND, int ACC, int FN>
+__device__ __forceinline__ void zero_rows(const FewArgs& a, int64_t drow, int f, int from, int to) {
+  const float zero[ACC] = {};
+  for (int k = from; k < to; ++k) put<KIND, ACC, FN>(a, drow + k, f, zero, false);
+}
+
 template <int KIND, int NT, int FN>
 __global__ void __launch_bounds__(kThreads, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const FewArgs a) {
@@ -176,12 +187,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 2 * BUFS);
   auto pfull_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + r); };
   auto pempty_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + kRing + r); };
+  auto jfull_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + 2 * kRing + r); };
+  auto jempty_bar = [&](int r) { return bar0 + 8u * (2 * STAGES + 2 * BUFS + 1 + 2 * kRing + kJoin + r); };
   unsigned char* misc = gbase + STAGES * F::STAGE + F::kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile unsigned* arrived = reinterpret_cast<volatile unsigned*>(misc + 8);
   volatile int* ring = reinterpret_cast<volatile int*>(misc + 16);
   Cuts* cuts = reinterpret_cast<Cuts*>(misc + 32);
+  volatile int4* joins = reinterpret_cast<volatile int4*>(misc + 64);    // Steps of written parts
   int* pre = reinterpret_cast<int*>(misc + F::kMisc);  // [E + 1] first tile of each expert
   int* rtiles = pre + (kMaxExperts + 1);               // [E] tiles of NT rows
   int* nrows = rtiles + kMaxExperts;                   // [E]
@@ -202,6 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; r < kRing; ++r) {
       mbar_init(pfull_bar(r), 1);
       mbar_init(pempty_bar(r), 5);             // the MMA thread and four epilogue warps
+    }
+    for (int r = 0; r < kJoin; ++r) {
+      mbar_init(jfull_bar(r), 128);
+      mbar_init(jempty_bar(r), 4);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -267,6 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const Cuts c = *cuts;
   const int npieces = (c.T - c.Ts) * c.P;
+  // training: the row of a tile up to which zeros follow its rows (its expert's last tile)
+  auto zero_to = [&](int n, int row0, int nvalid) {
+    return KIND == kUp && a.gu && row0 + nvalid == n ? (n + 63) / 64 * 64 - row0 : 0;
+  };
   auto piece = [&](int id) {                           // a fetched piece
     const int i = id / c.P, p = id - i * c.P;
     const int kb = KB * p / c.P;
@@ -448,24 +470,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue (warps 2..5)
     const int q = warp & 3;                    // TMEM lane quarter of this warp
     const int lane128 = q * 32 + lane;         // this thread's feature within a tile
     if (KIND == kDown) pdl_wait();             // the workspace is `up`'s until it has finished
-    int buf = 0;
+    int buf = 0, jn = 0;
     uint32_t bph = 0;
     bool ok = true;
+    // passes a written part (or, with len 0, the end) on to the joining warps
+    auto pass_on = [&](const Step& st) {
+      const int slot = jn % kJoin;
+      if (*abort_flag || !mbar_wait(jempty_bar(slot), ((jn / kJoin) & 1) ^ 1, a.err, a.limit_ns)) {
+        *abort_flag = 1;
+        ok = false;
+        return;
+      }
+      if (threadIdx.x == 64) {
+        joins[slot].x = st.t;
+        joins[slot].y = st.kb;
+        joins[slot].z = st.len;
+        joins[slot].w = st.piece;
+      }
+      mbar_arrive(jfull_bar(slot));            // after this thread's stores
+      ++jn;
+    };
     auto take = [&](const Step& st) {
       const Tile t = tile_at(st.t, pre, rtiles, a.E);
-      const int row0 = t.rt * NT, left = nrows[t.e] - row0;
-      const int nvalid = min(NT, left);
+      const int row0 = t.rt * NT, nvalid = min(NT, nrows[t.e] - row0);
       const bool whole = st.len == KB;
       const int f = t.nt * F::FEATURES + lane128;
       const int64_t drow = t.e * a.Cd + row0;
-      // training: the rows up to the next multiple of 64 are zeros (weight gradients reduce
-      // over whole blocks of 64)
-      const int nzero = KIND == kUp && a.gu && left <= NT ? (nrows[t.e] + 63) / 64 * 64 - row0 : 0;
       const int slot = st.piece >= 0 ? 2 * grid + st.piece : 2 * me + (st.kb == 0);
       float* part = a.part + (size_t)slot * (ACC * NT * 128) + lane128;
       const uint32_t tm0 = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -502,33 +537,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < ACC; ++j) sw[j] = wv[j];
           scales(i + AHEAD, xv, wv);
-          uint32_t v[ACC][NT / 16][16];
+          constexpr int AT_ONCE = ACC == 2 ? 1 : 2;       // 16-column groups in registers
 #pragma unroll
-          for (int k = 0; k < NT / 16; ++k)
-            if (k * 16 < nvalid) {
+          for (int k0 = 0; k0 < NT / 16; k0 += AT_ONCE) {
+          uint32_t v[ACC][AT_ONCE][16];
 #pragma unroll
-              for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm0 + buf * (ACC * NT) + j * NT + k * 16, v[j][k]);
+          for (int k = 0; k < AT_ONCE; ++k)
+            if ((k0 + k) * 16 < nvalid) {
+#pragma unroll
+              for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm0 + buf * (ACC * NT) + j * NT + (k0 + k) * 16, v[j][k]);
             }
           tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty_bar(buf));
-          if (++buf == BUFS) {
-            buf = 0;
-            bph ^= 1u;
+          if (k0 + AT_ONCE == NT / 16) {       // the last columns are here: hand the buffer back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
           }
 #pragma unroll
-          for (int k = 0; k < NT / 16; ++k)
-            if (k * 16 < nvalid) {
+          for (int k = 0; k < AT_ONCE; ++k)
+            if ((k0 + k) * 16 < nvalid) {
 #pragma unroll
               for (int i2 = 0; i2 < 16; ++i2) {
-                const int col = k * 16 + i2;
+                const int col = (k0 + k) * 16 + i2;
                 const float s = __shfl_sync(0xffffffffu, sx[col / 32], col % 32);
 #pragma unroll
                 for (int j = 0; j < ACC; ++j)
                   sum[j][col] = fmaf(s * sw[j], __uint_as_float(v[j][k][i2]), sum[j][col]);
               }
             }
+          }
+          if (++buf == BUFS) {
+            buf = 0;
+            bph ^= 1u;
+          }
         };
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) scales(d, x[d], w[d]);
@@ -586,76 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bph ^= 1u;
         }
       }
-      bool finish = whole;
-      if (!whole) {
-        // a part of a tile: the last one to come adds them all, in the order of the depth
-        int first, parts, counter;
-        if (st.piece >= 0) {
-          const int i = st.t - c.Ts;
-          first = 2 * grid + i * c.P;
-          parts = c.P;
-          counter = grid + i;
-        } else {
-          const long long U = (long long)c.Ts * KB, u = (long long)st.t * KB;
-          const int i0 = share_owner(U, c.G, u);
-          parts = share_owner(U, c.G, u + KB - 1) - i0 + 1;
-          first = 2 * i0 + 1;                  // the tile's first CTA, then slot 0 of the next ones
-          counter = i0;
-        }
-        epi_sync();
-        if (threadIdx.x == 64) {
-          __threadfence();
-          const unsigned before = atomicAdd(a.count + counter, 1u);
-          __threadfence();
-          if (before == (unsigned)parts - 1u) a.count[counter] = 0u;
-          *arrived = before;
-        }
-        epi_sync();
-        finish = *arrived == (unsigned)parts - 1u;
-        if (finish) {
-          const float* p0 = a.part + (size_t)first * (ACC * NT * 128) + lane128;
-          // from one part's slot to the next: 1 for pieces; for shares 2 i0 + 1, 2 i0 + 2, 2 i0 + 4, ...
-          auto at = [&](int i) {
-            const int d = st.piece >= 0 ? i : i == 0 ? 0 : 2 * i - 1;
-            return p0 + (size_t)d * (ACC * NT * 128);
-          };
-#pragma unroll 1
-          for (int c0 = 0; c0 < nvalid; c0 += 8) {
-            float s[ACC][8] = {};
-#pragma unroll 1
-            for (int i = 0; i < parts; i += 4) {         // four parts' loads in flight
-              float v[4][ACC][8];
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                const float* p = at(i + d);
-#pragma unroll
-                for (int j = 0; j < ACC; ++j)
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    v[d][j][k] = i + d < parts && c0 + k < nvalid ? __ldcg(p + (j * NT + c0 + k) * 128) : 0.f;
-              }
-#pragma unroll
-              for (int d = 0; d < 4; ++d)
-#pragma unroll
-                for (int j = 0; j < ACC; ++j)
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) s[j][k] += v[d][j][k];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (c0 + k < nvalid) {
-                float v[ACC];
-#pragma unroll
-                for (int j = 0; j < ACC; ++j) v[j] = s[j][k];
-                put<KIND, ACC, FN>(a, drow + c0 + k, f, v, true);
-              }
-          }
-        }
-      }
-      if (KIND == kUp && finish) {
-        const float zero[ACC] = {};
-        for (int k = nvalid; k < nzero; ++k) put<KIND, ACC, FN>(a, drow + k, f, zero, false);
-      }
+      if (!whole) pass_on(st);
+      else if (KIND == kUp) zero_rows<KIND, ACC, FN>(a, drow, f, nvalid, zero_to(nrows[t.e], row0, nvalid));
     };
     int t = c.t0, kb = c.kb0, left = c.len;
     while (ok && left > 0) {
@@ -678,6 +651,92 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (id >= npieces) break;
         take(piece(id));
       }
+    if (ok) pass_on(Step{0, 0, 0, 0});
+  } else {
+    // ------------------------------------------------------------ joining parts (warps 6..9)
+    const int lane128 = (warp - 6) * 32 + lane;
+    if (KIND == kDown) pdl_wait();
+    for (int jn = 0;; ++jn) {
+      const int slot = jn % kJoin;
+      // a part comes when its depth has been read: a whole share may lie before the first one
+      bool got = false;
+      for (int tries = 0; !got && tries < 8 && !*abort_flag; ++tries) got = mbar_poll(jfull_bar(slot), (jn / kJoin) & 1, a.limit_ns);
+      if (!got) {
+        if (!*abort_flag && lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
+        break;
+      }
+      const Step st{joins[slot].x, joins[slot].y, joins[slot].z, joins[slot].w};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(jempty_bar(slot));
+      if (st.len == 0) break;
+      // the last part of a tile to come adds them all, in the order of the depth
+      int first, parts, counter;
+      if (st.piece >= 0) {
+        const int i = st.t - c.Ts;
+        first = 2 * grid + i * c.P;
+        parts = c.P;
+        counter = grid + i;
+      } else {
+        const long long U = (long long)c.Ts * KB, u = (long long)st.t * KB;
+        const int i0 = share_owner(U, c.G, u);
+        parts = share_owner(U, c.G, u + KB - 1) - i0 + 1;
+        first = 2 * i0 + 1;                  // the tile's first CTA, then slot 0 of the next ones
+        counter = i0;
+      }
+      if (lane128 == 0) {
+        __threadfence();
+        const unsigned before = atomicAdd(a.count + counter, 1u);
+        __threadfence();
+        if (before == (unsigned)parts - 1u) a.count[counter] = 0u;
+        *arrived = before;
+      }
+      join_sync();
+      const bool finish = *arrived == (unsigned)parts - 1u;
+      join_sync();                           // all have read it
+      if (!finish) continue;
+      const Tile t = tile_at(st.t, pre, rtiles, a.E);
+      const int row0 = t.rt * NT, nvalid = min(NT, nrows[t.e] - row0);
+      const int f = t.nt * F::FEATURES + lane128;
+      const int64_t drow = t.e * a.Cd + row0;
+      const float* p0 = a.part + (size_t)first * (ACC * NT * 128) + lane128;
+      // from one part's slot to the next: 1 for pieces; for shares 2 i0 + 1, 2 i0 + 2, 2 i0 + 4, ...
+      auto at = [&](int i) {
+        const int d = st.piece >= 0 ? i : i == 0 ? 0 : 2 * i - 1;
+        return p0 + (size_t)d * (ACC * NT * 128);
+      };
+#pragma unroll 1
+      for (int c0 = 0; c0 < nvalid; c0 += 8) {
+        float s[ACC][8] = {};
+#pragma unroll 1
+        for (int i = 0; i < parts; i += 4) {         // four parts' loads in flight
+          float v[4][ACC][8];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const float* p = at(i + d);
+#pragma unroll
+            for (int j = 0; j < ACC; ++j)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                v[d][j][k] = i + d < parts && c0 + k < nvalid ? __ldcg(p + (j * NT + c0 + k) * 128) : 0.f;
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int j = 0; j < ACC; ++j)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) s[j][k] += v[d][j][k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c0 + k < nvalid) {
+            float v[ACC];
+#pragma unroll
+            for (int j = 0; j < ACC; ++j) v[j] = s[j][k];
+            put<KIND, ACC, FN>(a, drow + c0 + k, f, v, true);
+          }
+      }
+      if (KIND == kUp) zero_rows<KIND, ACC, FN>(a, drow, f, nvalid, zero_to(nrows[t.e], row0, nvalid));
+    }
   }
 
   tc_fence_before();
