@@ -23,6 +23,8 @@
 // accumulators of the next pieces must not wait for.  For 8-bit weights they do so after every
 // block, since its scales differ: acc += (xs ws) * block, as in fp8.cu.  `down` starts its
 // weight loads while `up` drains; only the loads of h wait for it.  Every wait is bounded.
+#include <type_traits>
+
 #include "common.cuh"
 #include "glu.cuh"
 #include "internal.h"
@@ -139,6 +141,14 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Arrival of a part: orders the part's stores (which the joining warps' mbarrier has brought
+// before it) ahead of it, and the loads of the other parts behind it.
+__device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // The four joining warps meet.
@@ -684,9 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         counter = i0;
       }
       if (lane128 == 0) {
-        __threadfence();
-        const unsigned before = atomicAdd(a.count + counter, 1u);
-        __threadfence();
+        const unsigned before = atom_add_acq_rel(a.count + counter, 1u);
         if (before == (unsigned)parts - 1u) a.count[counter] = 0u;
         *arrived = before;
       }
@@ -704,37 +712,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = st.piece >= 0 ? i : i == 0 ? 0 : 2 * i - 1;
         return p0 + (size_t)d * (ACC * NT * 128);
       };
+      // COLS columns at a time, PARTS of their parts in flight
+      auto add = [&](auto cols, auto pcs) {
+        constexpr int COLS = decltype(cols)::value, PARTS = decltype(pcs)::value;
 #pragma unroll 1
-      for (int c0 = 0; c0 < nvalid; c0 += 8) {
-        float s[ACC][8] = {};
+        for (int c0 = 0; c0 < nvalid; c0 += COLS) {
+          float s[ACC][COLS] = {};
 #pragma unroll 1
-        for (int i = 0; i < parts; i += 4) {         // four parts' loads in flight
-          float v[4][ACC][8];
+          for (int i = 0; i < parts; i += PARTS) {
+            float v[PARTS][ACC][COLS];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const float* p = at(i + d);
+            for (int d = 0; d < PARTS; ++d) {
+              const float* p = at(i + d);
 #pragma unroll
-            for (int j = 0; j < ACC; ++j)
+              for (int j = 0; j < ACC; ++j)
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                v[d][j][k] = i + d < parts && c0 + k < nvalid ? __ldcg(p + (j * NT + c0 + k) * 128) : 0.f;
+                for (int k = 0; k < COLS; ++k)
+                  v[d][j][k] = i + d < parts && c0 + k < nvalid ? __ldcg(p + (j * NT + c0 + k) * 128) : 0.f;
+            }
+#pragma unroll
+            for (int d = 0; d < PARTS; ++d)
+#pragma unroll
+              for (int j = 0; j < ACC; ++j)
+#pragma unroll
+                for (int k = 0; k < COLS; ++k) s[j][k] += v[d][j][k];
           }
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
+          for (int k = 0; k < COLS; ++k)
+            if (c0 + k < nvalid) {
+              float v[ACC];
 #pragma unroll
-            for (int j = 0; j < ACC; ++j)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) s[j][k] += v[d][j][k];
+              for (int j = 0; j < ACC; ++j) v[j] = s[j][k];
+              put<KIND, ACC, FN>(a, drow + c0 + k, f, v, true);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c0 + k < nvalid) {
-            float v[ACC];
-#pragma unroll
-            for (int j = 0; j < ACC; ++j) v[j] = s[j][k];
-            put<KIND, ACC, FN>(a, drow + c0 + k, f, v, true);
-          }
-      }
+      };
+      if (nvalid <= 2) add(std::integral_constant<int, 2>{}, std::integral_constant<int, 16>{});
+      else add(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
       if (KIND == kUp) zero_rows<KIND, ACC, FN>(a, drow, f, nvalid, zero_to(nrows[t.e], row0, nvalid));
     }
   }
