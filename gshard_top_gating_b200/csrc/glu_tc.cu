@@ -20,9 +20,11 @@
 // with Cp a multiple of 256, and the rows of an expert's last tile past n are stored as
 // zeros in training, since the weight gradients reduce over whole blocks of 64 rows.
 //
-// Roles per CTA (192 threads): warp 0 loads (TMA), warp 1 issues MMAs (the pair's first CTA)
-// and owns TMEM, warps 2..5 drain the accumulator, double buffered, while the next tile's
-// products run.  Every wait is bounded.
+// Roles per CTA: warp 0 loads (TMA), warp 1 issues MMAs (the pair's first CTA) and owns TMEM,
+// warps 2..5 drain the accumulator, double buffered, while the next tile's products run; in
+// `dh`, whose epilogue evaluates f and f' and moves four more tiles, warps 2..9, each 128
+// columns (with four warps it outlasted the products: 545 against 346 us for 8 x 2048 rows,
+// M = 2048, H = 8192).  Every wait is bounded.
 #include "common.cuh"
 #include "glu.cuh"
 #include "internal.h"
@@ -34,7 +36,8 @@ namespace {
 
 constexpr int BK = 64;                 // depth of a stage
 constexpr int PM = 256, PN = 256;      // pair tile
-constexpr int kThreads = 192;
+constexpr int epi_warps(int mode) { return mode == 3 ? 8 : 4; }     // kDh: 8
+constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 constexpr uint32_t A_BYTES = 128 * BK * 2;            // 16 KB: 128 rows of A
 constexpr uint32_t B_BYTES = 128 * BK * 2;            // 16 KB: 128 columns of B
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;   // per CTA
@@ -44,14 +47,14 @@ constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;        // shared::cluster address
 
 enum { kUp = 0, kUpSave = 1, kDown = 2, kDh = 3, kDx = 4, kDw = 5 };
 
-// Store tiles per epilogue warp: h; h, g and u; one; two buffers of (g, u), which dg and du
-// leave through; one; one.
-constexpr int store_tiles(int mode) { return mode == kUpSave ? 3 : mode == kDh ? 4 : 1; }
+// Store tiles per epilogue warp: h; h, g and u; one; two buffers of (g, u) of 32 columns, which
+// dg and du leave through; one; one.
+constexpr int store_tiles(int mode) { return mode == kUpSave ? 3 : mode == kDh ? 2 : 1; }
 constexpr int stages(int mode) { return mode == kUpSave ? 5 : mode == kDh ? 4 : 6; }
 constexpr uint32_t kBars = 512;
 constexpr size_t smem_bytes(int mode) {
   // alignment slack, stages, store tiles, barriers, misc, tile tables
-  return 1024 + (size_t)stages(mode) * STAGE_BYTES + 4 * store_tiles(mode) * TILE_BYTES + kBars + 16 +
+  return 1024 + (size_t)stages(mode) * STAGE_BYTES + epi_warps(mode) * store_tiles(mode) * TILE_BYTES + kBars + 16 +
          4 * (3 * kMaxExperts + 1);
 }
 // A CTA owns its SM (see the expert GEMMs of ffn_tc.cu): no other TMEM user fits beside it.
@@ -90,17 +93,6 @@ __device__ __forceinline__ void put_half(uint32_t tile, int lane, int half, cons
     st_shared_v4(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
                  pk[4 * j + 3]);
 }
-__device__ __forceinline__ void get_half(uint32_t tile, int lane, int half, uint32_t (&pk)[16]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 v = ld_shared_v4(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4));
-    pk[4 * j] = v.x;
-    pk[4 * j + 1] = v.y;
-    pk[4 * j + 2] = v.z;
-    pk[4 * j + 3] = v.w;
-  }
-}
-
 // Plain output of one warp: 32 rows x 256 columns from column col0 (N columns, a multiple
 // of 64), nvalid of the rows kept (and row stores where that is fewer than 32).
 __device__ __forceinline__ void store_plain(const CUtensorMap* tmD, uint32_t tmem, uint32_t tile, int64_t row0, int col0,
@@ -193,16 +185,34 @@ __device__ __forceinline__ void store_up(const CUtensorMap* tmD, const CUtensorM
   }
 }
 
-// The g and u chunk (64 columns) that starts at column col, by TMA into a pair of tiles.
+// 32 packed bf16 of this lane's row in a 32-column tile with 64-byte swizzle.
+constexpr uint32_t NARROW_BYTES = 2048;
+__device__ __forceinline__ void put_narrow(uint32_t tile, int lane, const uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    st_shared_v4(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+}
+__device__ __forceinline__ void get_narrow(uint32_t tile, int lane, uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = ld_shared_v4(tile + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+    pk[4 * j] = v.x;
+    pk[4 * j + 1] = v.y;
+    pk[4 * j + 2] = v.z;
+    pk[4 * j + 3] = v.w;
+  }
+}
+
+// g and u of 32 columns from column col, by TMA into a pair of narrow tiles.
 __device__ __forceinline__ void load_gu(const CUtensorMap* tmGU, uint32_t tile, uint32_t bar, int row0, int col, int H) {
-  mbar_arrive_expect_tx(bar, 2 * TILE_BYTES);
+  mbar_arrive_expect_tx(bar, 2 * NARROW_BYTES);
   tma_load_2d(tile, tmGU, bar, col, row0);
-  tma_load_2d(tile + TILE_BYTES, tmGU, bar, H + col, row0);
+  tma_load_2d(tile + NARROW_BYTES, tmGU, bar, H + col, row0);
 }
 
 // MODE kUp, kUpSave, kDown, kDh, kDx.  tmD2: kUpSave the [g|u] output, kDh the [g|u] input.
 template <int MODE, int FN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     glu_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD2,
                     const PairArgs a) {
@@ -215,14 +225,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
   unsigned char* gbase = smem_raw + (base - raw_base);
   const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
-  const uint32_t bar0 = tiles0 + 4 * store_tiles(MODE) * TILE_BYTES;
+  const uint32_t bar0 = tiles0 + epi_warps(MODE) * store_tiles(MODE) * TILE_BYTES;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
   auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
   auto gu_bar = [&](int w, int i) { return bar0 + 8u * (2 * STAGES + 5 + 2 * w + i); };
-  unsigned char* misc = gbase + STAGES * STAGE_BYTES + 4 * store_tiles(MODE) * TILE_BYTES + kBars;
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + epi_warps(MODE) * store_tiles(MODE) * TILE_BYTES + kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   int* tile_pre = reinterpret_cast<int*>(misc + 16);   // [E + 1]
@@ -243,11 +253,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 2 * 128);       // epilogue threads of both CTAs
+      mbar_init(tempty_bar(i), 2 * epi_warps(MODE));       // epilogue warps of both CTAs
     }
     mbar_init(done_bar, 1);
     if (MODE == kDh)
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < 8; ++w)
         for (int i = 0; i < 2; ++i) mbar_init(gu_bar(w, i), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -375,8 +385,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5, both CTAs)
+    // ------------------------------------------------------------ epilogue (from warp 2, both CTAs)
     const int q = warp & 3;
+    const int part = (warp - 2) >> 2;            // kDh: which 128 of the tile's 256 columns
     const uint32_t tile0 = tiles0 + (warp - 2) * store_tiles(MODE) * TILE_BYTES;
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, i = 0;
@@ -387,14 +398,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int local = mt * PM + (int)rank * 128 + q * 32;     // row within the expert
       const int64_t row0 = e * a.Cd + local;
       const int nvalid = min(32, nrows[e] - local);
-      const int col0 = nt * COLS;
-      if (MODE == kDh && nvalid > 0 && lane == 0) {
+      const int col0 = nt * COLS + part * 128;
+      if (MODE == kDh && nvalid > 0 && col0 < a.N && lane == 0) {
         bulk_wait_read0();       // the previous tile's stores have read their buffers
         load_gu(&tmD2, tile0, gu_bar(warp - 2, 0), (int)row0, col0, a.N);
+        // the other columns into L2 while the products run
+        for (int b = 1; b < 4 && col0 + b * 32 < a.N; ++b) {
+          tma_prefetch_l2_2d(&tmD2, col0 + b * 32, (int)row0);
+          tma_prefetch_l2_2d(&tmD2, a.N + col0 + b * 32, (int)row0);
+        }
       }
       if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
         *abort_flag = 1;
-        if (MODE == kDh && nvalid > 0) mbar_wait(gu_bar(warp - 2, 0), gph & 1u, a.err, a.limit_ns);
+        if (MODE == kDh && nvalid > 0 && col0 < a.N) mbar_wait(gu_bar(warp - 2, 0), gph & 1u, a.err, a.limit_ns);
         break;
       }
       tc_fence_after();
@@ -404,65 +420,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           store_up<FN, MODE == kUpSave>(&tmD, &tmD2, tm, tile0, (int)row0, col0, a.N, nvalid, lane);
       } else if constexpr (MODE == kDh) {
         bool ok = true;
-        const int nb = min(PN / 64, (a.N - col0 + 63) / 64);
+        const int nb = max(0, min(4, (a.N - col0) / 32));      // N is a multiple of 64
         if (nvalid > 0) {
 #pragma unroll 1
           for (int b = 0; b < nb; ++b) {
-            const uint32_t buf = tile0 + (b & 1) * 2 * TILE_BYTES;
+            const uint32_t buf = tile0 + (b & 1) * 2 * NARROW_BYTES;
             if (b + 1 < nb && lane == 0) {
-              // the other buffer's stores (chunk b - 1) have left; bring in chunk b + 1
+              // the other buffer's stores (columns b - 1) have left; bring in the next ones
               bulk_wait_read0();
-              load_gu(&tmD2, tile0 + ((b + 1) & 1) * 2 * TILE_BYTES, gu_bar(warp - 2, (b + 1) & 1), (int)row0,
-                      col0 + (b + 1) * 64, a.N);
+              load_gu(&tmD2, tile0 + ((b + 1) & 1) * 2 * NARROW_BYTES, gu_bar(warp - 2, (b + 1) & 1), (int)row0,
+                      col0 + (b + 1) * 32, a.N);
             }
             __syncwarp();
+            uint32_t r[32], pg[16], pu[16];
+            tmem_ld_32x32b_x32(tm + part * 128 + b * 32, r);
             ok = ok && mbar_wait(gu_bar(warp - 2, b & 1), (gph >> (b & 1)) & 1u, a.err, a.limit_ns);
             gph ^= 1u << (b & 1);
+            get_narrow(buf, lane, pg);
+            get_narrow(buf + NARROW_BYTES, lane, pu);
+            tmem_ld_wait();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t r[32], pg[16], pu[16];
-              get_half(buf, lane, half, pg);
-              get_half(buf + TILE_BYTES, lane, half, pu);
-              tmem_ld_32x32b_x32(tm + b * 64 + half * 32, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float d0 = __uint_as_float(r[2 * j]), d1 = __uint_as_float(r[2 * j + 1]);
-                float f0, df0, f1, df1;
-                glu_f_df<FN, true>(bf16lo(pg[j]), f0, df0);
-                glu_f_df<FN, true>(bf16hi(pg[j]), f1, df1);
-                const float u0 = bf16lo(pu[j]), u1 = bf16hi(pu[j]);
-                pg[j] = lane < nvalid ? pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1) : 0u;
-                pu[j] = lane < nvalid ? pack_bf16x2(d0 * f0, d1 * f1) : 0u;
-              }
-              put_half(buf, lane, half, pg);
-              put_half(buf + TILE_BYTES, lane, half, pu);
+            for (int j = 0; j < 16; ++j) {
+              const float d0 = __uint_as_float(r[2 * j]), d1 = __uint_as_float(r[2 * j + 1]);
+              float f0, df0, f1, df1;
+              glu_f_df<FN, true>(bf16lo(pg[j]), f0, df0);
+              glu_f_df<FN, true>(bf16hi(pg[j]), f1, df1);
+              const float u0 = bf16lo(pu[j]), u1 = bf16hi(pu[j]);
+              pg[j] = lane < nvalid ? pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1) : 0u;
+              pu[j] = lane < nvalid ? pack_bf16x2(d0 * f0, d1 * f1) : 0u;
             }
+            put_narrow(buf, lane, pg);
+            put_narrow(buf + NARROW_BYTES, lane, pu);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d_hint(&tmD, buf, col0 + b * 64, (int)row0, l2_policy_evict_first());
-              tma_store_2d_hint(&tmD, buf + TILE_BYTES, a.N + col0 + b * 64, (int)row0, l2_policy_evict_first());
+              tma_store_2d_hint(&tmD, buf, col0 + b * 32, (int)row0, l2_policy_evict_first());
+              tma_store_2d_hint(&tmD, buf + NARROW_BYTES, a.N + col0 + b * 32, (int)row0, l2_policy_evict_first());
               bulk_commit();
             }
           }
-        } else {
+        } else if (nb > 0) {
           // rows past the last one in this tile: zeros, so that the block that holds it reduces
           // over nothing else
-#pragma unroll 1
-          for (int b = 0; b < nb; ++b) {
-            if (lane == 0) bulk_wait_read0();
-            __syncwarp();
-            const uint32_t z[16] = {};
-            put_half(tile0, lane, 0, z);
-            put_half(tile0, lane, 1, z);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d_hint(&tmD, tile0, col0 + b * 64, (int)row0, l2_policy_evict_first());
-              tma_store_2d_hint(&tmD, tile0, a.N + col0 + b * 64, (int)row0, l2_policy_evict_first());
-              bulk_commit();
+          if (lane == 0) bulk_wait_read0();
+          __syncwarp();
+          const uint32_t z[16] = {};
+          put_narrow(tile0, lane, z);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            for (int b = 0; b < nb; ++b) {
+              tma_store_2d_hint(&tmD, tile0, col0 + b * 32, (int)row0, l2_policy_evict_first());
+              tma_store_2d_hint(&tmD, tile0, a.N + col0 + b * 32, (int)row0, l2_policy_evict_first());
             }
+            bulk_commit();
           }
         }
         if (!ok) *abort_flag = 1;
@@ -470,8 +481,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (nvalid > 0) store_plain(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
       }
       tc_fence_before();
-      if (leader) mbar_arrive(tempty_bar(acc));
-      else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
+      }
     }
     if (lane == 0) bulk_wait0();
     __syncwarp();
@@ -489,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Weight gradients D[e] = A[e, :n]^T B[e, :n] ([P, N] per expert): both operands with their
 // rows as the depth.  Rows n .. ceil64(n) - 1 of an operand hold zeros, or its last, partial
 // block is read from a tail copy ([E, 64, width], zero-filled; tailA / tailB).
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     glu_dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmAt,
                   const __grid_constant__ CUtensorMap tmBt, const PairArgs a) {
@@ -524,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 2 * 128);
+      mbar_init(tempty_bar(i), 2 * epi_warps(kDw));
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -657,8 +671,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     32, zero, nullptr, lane);
       if (!zero) {
         tc_fence_before();
-        if (leader) mbar_arrive(tempty_bar(acc));
-        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(tempty_bar(acc));
+          else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
+        }
       }
     }
     if (lane == 0) bulk_wait0();
@@ -699,7 +716,7 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   const size_t smem = smem_bytes(MODE);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), smem, a.st, tmA, tmB, tmD, tmD2, p);
+  return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(threads(MODE)), smem, a.st, tmA, tmB, tmD, tmD2, p);
 }
 
 template <int MODE>
@@ -741,7 +758,7 @@ cudaError_t launch_dw(const GluArgs& a, const void* A, int64_t Ca, int P, const 
   const size_t smem = smem_bytes(kDw);
   cudaError_t e = cudaFuncSetAttribute(glu_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(kThreads), smem, a.st, tmA, tmB, tmD, tmAt, tmBt, p);
+  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(threads(kDw)), smem, a.st, tmA, tmB, tmD, tmAt, tmBt, p);
 }
 
 }  // namespace
@@ -786,8 +803,8 @@ cudaError_t glu_dh_bf16(const GluArgs& a) {
   CUtensorMap tmA, tmB, tmD, tmG;
   if (!encode_2d(&tmA, a.dy, a.M, rows(a.E, a.C), BK, 128) ||
       !encode_2d(&tmB, a.W2, a.M, rows(a.E, a.H), BK, 128) ||
-      !encode_2d(&tmD, a.dgu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 64, 32) ||
-      !encode_2d(&tmG, a.gu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 64, 32))
+      !encode_2d_narrow(&tmD, a.dgu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 32) ||
+      !encode_2d_narrow(&tmG, a.gu, 2 * (uint64_t)a.H, rows(a.E, a.Cp), 32))
     return cudaErrorInvalidValue;
   PairArgs p = pair_args(a);
   p.Ca = a.C;

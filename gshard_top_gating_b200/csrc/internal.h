@@ -46,6 +46,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // 0 = dense), bf16 or fp32, 128-byte swizzle.
 bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_in,
                uint32_t box_out, bool f32 = false, uint64_t pitch = 0);
+// bf16 in boxes of 32 columns, 64-byte swizzle, dense.
+bool encode_2d_narrow(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_out);
 // bf16 matrix of `rows` x `cols` (a multiple of 64) seen as {64 columns, rows, blocks of 64
 // columns}, box {64, 64, blocks}: 64 * blocks columns of 64 rows in one load, as 64 x 64 tiles.
 bool encode_column_blocks(CUtensorMap* tm, const void* ptr, uint64_t cols, uint64_t rows, uint32_t blocks);

@@ -21,7 +21,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool encode(CUtensorMap* tm, CUtensorMapDataType type, uint64_t es, const void* ptr, uint64_t inner,
-            uint64_t outer, uint32_t box_in, uint32_t box_out, uint64_t pitch) {
+            uint64_t outer, uint32_t box_in, uint32_t box_out, uint64_t pitch,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer};
@@ -29,8 +30,7 @@ bool encode(CUtensorMap* tm, CUtensorMapDataType type, uint64_t es, const void* 
   cuuint32_t box[2] = {box_in, box_out};
   cuuint32_t estr[2] = {1, 1};
   return fn(tm, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -39,6 +39,10 @@ bool encode_2d(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer,
                uint32_t box_out, bool f32, uint64_t pitch) {
   return encode(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2, ptr,
                 inner, outer, box_in, box_out, pitch);
+}
+
+bool encode_2d_narrow(CUtensorMap* tm, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_out) {
+  return encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, inner, outer, 32, box_out, 0, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool encode_column_blocks(CUtensorMap* tm, const void* ptr, uint64_t cols, uint64_t rows, uint32_t blocks) {
