@@ -34,50 +34,70 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
 
+// Eight consecutive values as they are stored: 16 bytes of bf16, 32 of fp32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8]) {
-  if (BF16) {
-    const uint4 r = ld_nc_v4(static_cast<const char*>(x) + i * 2);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw8 {
+  uint4 r[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* x, int64_t i) {
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) r[h] = ld_nc_v4(static_cast<const char*>(x) + i * (BF16 ? 2 : 4) + h * 16);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) r[h] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+    const uint4 q = r[BF16 ? 0 : 1];
+    const uint32_t z[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16lo(w[j]);
-      v[2 * j + 1] = bf16hi(w[j]);
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 r = ld_nc_v4(static_cast<const char*>(x) + i * 4 + h * 16);
-      v[4 * h] = __uint_as_float(r.x);
-      v[4 * h + 1] = __uint_as_float(r.y);
-      v[4 * h + 2] = __uint_as_float(r.z);
-      v[4 * h + 3] = __uint_as_float(r.w);
+      v[BF16 ? 2 * j : j] = BF16 ? bf16lo(w[j]) : __uint_as_float(w[j]);
+      v[BF16 ? 2 * j + 1 : 4 + j] = BF16 ? bf16hi(w[j]) : __uint_as_float(z[j]);
     }
   }
-}
+};
 
-// 16 lanes per block of 128 values, 8 values each.
-template <bool BF16>
+// 16 lanes per block of 128 values, 8 values each; BLOCKS blocks of one lane group are loaded
+// before the first is used.  EVEN: K is a multiple of 128, so block b starts at value 128 b.
+template <bool BF16, bool EVEN, int BLOCKS>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restrict__ x, uint2* __restrict__ q,
                                                             float* __restrict__ s, uint32_t nblocks, uint32_t KB, int K) {
   pdl_wait();
   const uint32_t lane = threadIdx.x & 15;
-  for (uint32_t b = blockIdx.x * 16u + threadIdx.x / 16u; b < nblocks; b += gridDim.x * 16u) {
-    const uint32_t row = b / KB, kb = b - row * KB;
-    const int k = (int)(kb * 128u + lane * 8u);
-    const int64_t i = (int64_t)row * K + k;
-    float v[8] = {};
-    if (k < K) load8<BF16>(x, i, v);
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+  // first value of this lane in block b, or -1 (past the row's end)
+  auto at = [&](uint32_t b) -> int64_t {
+    if (EVEN) return (int64_t)b * 128 + lane * 8u;
+    const uint32_t row = b / KB, k = (b - row * KB) * 128u + lane * 8u;
+    return k < (uint32_t)K ? (int64_t)row * K + k : -1;
+  };
+  const uint32_t group = blockIdx.x * 16u + threadIdx.x / 16u;
+  const uint32_t b0 = group * BLOCKS;
+  Raw8<BF16> raw[BLOCKS];
+#pragma unroll
+  for (int u = 0; u < BLOCKS; ++u) {
+    raw[u].zero();
+    if (b0 + u < nblocks) {
+      const int64_t i = at(b0 + u);
+      if (i >= 0) raw[u].load(x, i);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < BLOCKS; ++u) {
+    if (b0 + u >= nblocks) break;                     // the same for all lanes of a group
+    float v[8];
+    raw[u].get(v);
     float a = kTiny;
 #pragma unroll
     for (int j = 0; j < 8; ++j) a = amax2(a, v[j]);
-    const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a = amax2(a, __shfl_xor_sync(mask, a, o));
     const float r = __fdiv_rn(kMax, a);
-    if (k < K)
+    const int64_t i = at(b0 + u);
+    if (i >= 0)
       q[i / 8] = make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
-    if (lane == 0) s[b] = __fdiv_rn(a, kMax);
+    if (lane == 0) s[b0 + u] = __fdiv_rn(a, kMax);
   }
 }
 
@@ -95,7 +115,11 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* __res
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const int k = k0 + kr + 16 * r;
-    if (k < K && n < N) load8<BF16>(W, ((int64_t)e * K + k) * N + n, v[r]);
+    if (k < K && n < N) {
+      Raw8<BF16> raw;
+      raw.load(W, ((int64_t)e * K + k) * N + n);
+      raw.get(v[r]);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) a = amax2(a, v[r][j]);
   }
@@ -124,14 +148,25 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* __res
   }
 }
 
+template <bool BF16, bool EVEN>
+cudaError_t launch_rows(uint32_t nblocks, uint32_t KB, int K, const void* x, void* q, float* s, cudaStream_t st) {
+  // many blocks: several in flight per lane group (65536 x 7168 bf16: 267 us with one, 244 with
+  // two, 229 with four, 224 with eight; copying the same bytes 218); few: one each, on more SMs
+  constexpr int MANY = BF16 ? 8 : 4;
+  const bool many = nblocks >= 148u * 128u * MANY;
+  const uint32_t per = 16u * (many ? MANY : 1);
+  const dim3 grid((nblocks + per - 1) / per);
+  auto kern = many ? quantize_rows_kernel<BF16, EVEN, MANY> : quantize_rows_kernel<BF16, EVEN, 1>;
+  return launch_pdl(kern, grid, dim3(256), 0, st, x, static_cast<uint2*>(q), s, nblocks, KB, K);
+}
+
 }  // namespace
 
 cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* q, float* s, cudaStream_t st) {
   const uint32_t KB = (uint32_t)((K + 127) / 128), nblocks = (uint32_t)(R * KB);
-  const uint32_t want = (nblocks + 15) / 16;
-  const dim3 grid(want < 148 * 64 ? want : 148 * 64);
-  if (bf16) return launch_pdl(quantize_rows_kernel<true>, grid, dim3(256), 0, st, x, static_cast<uint2*>(q), s, nblocks, KB, K);
-  return launch_pdl(quantize_rows_kernel<false>, grid, dim3(256), 0, st, x, static_cast<uint2*>(q), s, nblocks, KB, K);
+  if (K % 128 == 0)
+    return bf16 ? launch_rows<true, true>(nblocks, KB, K, x, q, s, st) : launch_rows<false, true>(nblocks, KB, K, x, q, s, st);
+  return bf16 ? launch_rows<true, false>(nblocks, KB, K, x, q, s, st) : launch_rows<false, false>(nblocks, KB, K, x, q, s, st);
 }
 
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st) {

@@ -4,8 +4,8 @@
 //   C_e(i, j) = sum_k A_e(i, k) B_e(k, j)
 //
 // with the rows i (or, for the weight gradients, the depth k) limited to the n rows expert e
-// holds; rows past them are neither read nor written.  A tile of TM x TN results per block
-// of 256 threads, TM/16 x TN/16 each, depth in steps of 16 through shared memory with the
+// holds; rows past them are neither read nor written.  A tile of T x T results per block
+// of 256 threads, T/16 x T/16 each, depth in steps of TK through shared memory with the
 // next step's operands in registers meanwhile.  A thread's columns lie in two groups, one in
 // each half of the tile: in `up` the first half holds columns of Wg and the second the same
 // columns of Wu, so that g and u of an element meet in one thread.
@@ -16,7 +16,7 @@ namespace moe {
 
 namespace {
 
-constexpr int TK = 16, kThreads = 256;
+constexpr int kThreads = 256;
 enum { kSPlain = 0, kSUp = 1, kSDh = 2 };
 
 struct SimtArgs {
@@ -35,9 +35,14 @@ struct SimtArgs {
 
 // AT: A's rows are contiguous (A(i, k) at k * lda + i), else its depth (i * lda + k).
 // BT: B's depth is contiguous (B(k, j) at j * ldb + k), else its columns (k * ldb + j).
-template <int T, bool AT, bool BT, int EPI, int FN>
+template <int T, int TK, bool AT, bool BT, int EPI, int FN>
 __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
-  constexpr int R = T / 16, G = T / 32;       // rows and columns-per-group of a thread
+  // small tiles: four groups of 64 threads take a quarter of each step's depth each, so that
+  // every thread still has 4 x 4 results (with 2 x 2, shared-memory loads bound the step)
+  constexpr int KS = T == 32 ? 4 : 1, SIDE = T == 32 ? 8 : 16;
+  constexpr int R = T / SIDE, G = T / (2 * SIDE);       // rows and columns-per-half of a thread
+  pdl_wait();
+  pdl_trigger();
   const int e = blockIdx.z;
   const int n = min(max(g.n[e], 0), g.C);
   const int rows = g.rows ? g.rows : n, K = g.K ? g.K : n;
@@ -47,9 +52,11 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
   if (i0 >= rows || (g.skip_empty && n == 0)) return;
   const float* A = g.A + e * g.a_z;
   const float* B = g.B + e * g.b_z;
-  __shared__ __align__(16) float As[TK][T + 4];
-  __shared__ __align__(16) float Bs[TK][T + 4];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  __shared__ __align__(16) float shared[2][TK][T + 4];
+  auto& As = shared[0];
+  auto& Bs = shared[1];
+  const int tid = threadIdx.x, ks = tid / (SIDE * SIDE);
+  const int tx = tid % SIDE, ty = tid / SIDE % SIDE;
   constexpr int L = T * TK / (4 * kThreads);   // float4 loads per thread and operand
   float4 ra[L], rb[L];
 
@@ -110,7 +117,8 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
     __syncthreads();
     if (k0 + TK < K) load(k0 + TK);
 #pragma unroll
-    for (int k = 0; k < TK; ++k) {
+    for (int kk = 0; kk < TK / KS; ++kk) {
+      const int k = ks * (TK / KS) + kk;
       float av[R], bv[2 * G];
 #pragma unroll
       for (int r = 0; r < R; ++r) av[r] = As[k][ty * R + r];
@@ -127,11 +135,30 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
     __syncthreads();
   }
 
+  if constexpr (KS > 1) {
+    // the groups' sums meet in the operands' memory; group ks keeps row ks of each 4 x 4
+    static_assert(KS == R && KS * T * T <= 2 * TK * (T + 4), "the sums fit into the operands' memory");
+    float* sums = &shared[0][0][0];            // [group][thread][R][2 G]; the last step's reads are done
+    const int t0 = tid % (SIDE * SIDE);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < 2 * G; ++c) sums[((r * 2 * G + c) * KS + ks) * SIDE * SIDE + t0] = acc[r][c];
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2 * G; ++c) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) s += sums[((ks * 2 * G + c) * KS + k) * SIDE * SIDE + t0];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r][c] = s;      // one of the rows below is used: r = ks
+    }
+  }
   float* D = g.D + e * g.d_z;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = i0 + ty * R + r;
-    if (i >= rows) continue;
+    if (i >= rows || (KS > 1 && r != ks)) continue;
     if (EPI == kSUp) {
 #pragma unroll
       for (int c = 0; c < G; ++c) {
@@ -163,16 +190,19 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
   }
 }
 
-// 128 x 128 tiles when they fill the device twice over, else 64 x 64 (more blocks).
+// Tiles of 128 x 128 when they fill the device twice over, else of 64 x 64 when those fill it,
+// else of 32 x 32 with four times the depth per step: small products are bound by the
+// latency of their steps (a training step of 8 experts x 80 rows, M = 64, H = 256: 72 us with
+// 64 x 64 tiles of depth 16 throughout, 55 us).
 template <bool AT, bool BT, int EPI, int FN>
 cudaError_t launch(const SimtArgs& g, int64_t rows, int cols, int E, int num_sms, cudaStream_t st) {
-  const int64_t big = (rows + 127) / 128 * ((cols + 127) / 128) * E;
-  const int T = big >= 2 * num_sms ? 128 : 64;
+  auto tiles = [&](int T) { return (rows + T - 1) / T * ((cols + T - 1) / T) * E; };
+  const int T = tiles(128) >= 2 * num_sms ? 128 : tiles(64) >= num_sms ? 64 : 32;
   const int cw = EPI == kSUp ? T / 2 : T;
   const dim3 grid((cols / (EPI == kSUp ? 2 : 1) + cw - 1) / cw, (unsigned)((rows + T - 1) / T), E);
-  if (T == 128) glu_simt_kernel<128, AT, BT, EPI, FN><<<grid, kThreads, 0, st>>>(g);
-  else glu_simt_kernel<64, AT, BT, EPI, FN><<<grid, kThreads, 0, st>>>(g);
-  return cudaGetLastError();
+  if (T == 128) return launch_pdl(glu_simt_kernel<128, 16, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
+  if (T == 64) return launch_pdl(glu_simt_kernel<64, 16, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
+  return launch_pdl(glu_simt_kernel<32, 64, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
 }
 
 template <bool AT, bool BT, int EPI>
