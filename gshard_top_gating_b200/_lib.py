@@ -86,6 +86,8 @@ def _load() -> ctypes.CDLL:
         "moe_ep_check": [P, P],
     })
     sig.update({
+        "moe_create_gated": [ctypes.POINTER(P), I64, I64, I64, I32, I32, D, ctypes.c_int, ctypes.c_int, P, P, P, P],
+        "moe_create_gated_fp8": [ctypes.POINTER(P), I64, I64, I64, I32, I32, D, ctypes.c_int, P, P, P, P, P, P],
         "moe_glu_create": [ctypes.POINTER(P), I32, I64, I64, I64, ctypes.c_int, ctypes.c_int, P, P],
         "moe_glu_destroy": [P],
         "moe_glu_forward": [P, I64, P, P, P, P],
@@ -155,6 +157,22 @@ def moe_create(S_max, M, H, E, k, capacity_factor, act, Wg, gate_bias, W1, W2) -
     dt = MOE_BF16 if act in ("bf16", torch.bfloat16, MOE_BF16) else MOE_F32
     _check("moe_create", lib.moe_create(ctypes.byref(h), S_max, M, H, E, k, float(capacity_factor),
                                         dt, _ptr(Wg), _ptr(gate_bias), _ptr(W1), _ptr(W2)))
+    return h.value
+
+
+def moe_create_gated(S_max, M, H, E, k, capacity_factor, act, fn, Wg, gate_bias, W13, W2) -> int:
+    h = ctypes.c_void_p()
+    dt = MOE_BF16 if act in ("bf16", torch.bfloat16, MOE_BF16) else MOE_F32
+    _check("moe_create_gated", lib.moe_create_gated(ctypes.byref(h), S_max, M, H, E, k, float(capacity_factor), dt,
+                                                    int(fn), _ptr(Wg), _ptr(gate_bias), _ptr(W13), _ptr(W2)))
+    return h.value
+
+
+def moe_create_gated_fp8(S_max, M, H, E, k, capacity_factor, fn, Wg, gate_bias, W13q, W13s, W2q, W2s) -> int:
+    h = ctypes.c_void_p()
+    _check("moe_create_gated_fp8", lib.moe_create_gated_fp8(ctypes.byref(h), S_max, M, H, E, k, float(capacity_factor),
+                                                            int(fn), _ptr(Wg), _ptr(gate_bias), _ptr(W13q), _ptr(W13s),
+                                                            _ptr(W2q), _ptr(W2s)))
     return h.value
 
 

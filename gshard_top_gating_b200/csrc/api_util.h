@@ -39,6 +39,13 @@ inline bool on_device(int device) {
   return cudaGetDevice(&cur) == cudaSuccess && cur == device;
 }
 
+// Whether `st` is being captured into a graph; an error (a capture elsewhere in global mode)
+// counts as capturing.
+inline bool is_capturing(cudaStream_t st) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone;
+}
+
 // Synchronises `st`, reads a device error word and, if it is set, clears it and the words
 // behind it (`words` in all).
 inline moe_status take_device_error(unsigned* err, cudaStream_t st, size_t words = 1) {

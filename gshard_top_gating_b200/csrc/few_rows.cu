@@ -802,7 +802,7 @@ size_t few_rows_workspace(int64_t C_max, bool fp8, int num_sms, size_t* counts) 
 }
 
 cudaError_t glu_few_up(const GluArgs& a) {
-  const int nt = row_tile(a.C, kMostBf16);
+  const int nt = row_tile(a.rows, kMostBf16);
   CUtensorMap tmW, tmX;
   if (!encode_column_blocks(&tmW, a.W13, 2 * (uint64_t)a.H, (uint64_t)a.E * a.M, 2) ||
       !encode_2d(&tmX, a.x, a.M, (uint64_t)a.E * a.C, 64, nt))
@@ -828,7 +828,7 @@ cudaError_t glu_few_up(const GluArgs& a) {
 }
 
 cudaError_t glu_few_down(const GluArgs& a) {
-  const int nt = row_tile(a.C, kMostBf16);
+  const int nt = row_tile(a.rows, kMostBf16);
   CUtensorMap tmW, tmX;
   if (!encode_column_blocks(&tmW, a.W2, a.M, (uint64_t)a.E * a.H, 4) ||
       !encode_2d(&tmX, a.h, a.H, (uint64_t)a.E * a.Cp, 64, nt))
@@ -851,7 +851,7 @@ cudaError_t glu_few_down(const GluArgs& a) {
 }
 
 cudaError_t fp8_few(const Fp8Args& a) {
-  const int nt = row_tile(a.C, kMostFp8);
+  const int nt = row_tile(a.rows, kMostFp8);
   CUtensorMap tmW, tmX;
   if (!encode_2d_bytes(&tmW, a.wq, a.K, (uint64_t)a.E * a.N, 128, nt <= 32 ? 256 : 128) ||
       !encode_2d_bytes(&tmX, a.xq, a.K, (uint64_t)a.E * a.C, 128, nt))
@@ -874,5 +874,18 @@ cudaError_t fp8_few(const Fp8Args& a) {
   f.limit_ns = a.limit_ns;
   return launch_nt<kFp8, kGluSilu>(nt, tmW, tmX, f, a.num_sms, a.st);
 }
+
+// Both sides run both products of the gated experts alike, so that `down` finds `up` before it.
+cudaError_t glu_up(const GluArgs& a, bool bf16) {
+  if (!bf16) return glu_up_f32(a);
+  return a.rows <= kMostBf16 ? glu_few_up(a) : glu_up_bf16(a);
+}
+
+cudaError_t glu_down(const GluArgs& a, bool bf16) {
+  if (!bf16) return glu_down_f32(a);
+  return a.rows <= kMostBf16 ? glu_few_down(a) : glu_down_bf16(a);
+}
+
+cudaError_t fp8_matmul(const Fp8Args& a) { return a.rows <= kMostFp8 ? fp8_few(a) : fp8_pair(a); }
 
 }  // namespace moe

@@ -314,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t fp8_matmul(const Fp8Args& a) {
+cudaError_t fp8_pair(const Fp8Args& a) {
   CUtensorMap tmA, tmB, tmD;
   const uint64_t rows = (uint64_t)a.E * (uint64_t)a.C;
   if (!encode_2d_bytes(&tmA, a.xq, a.K, rows, BK, 128) || !encode_2d_bytes(&tmB, a.wq, a.K, (uint64_t)a.E * a.N, BK, 128) ||

@@ -102,7 +102,7 @@ moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq, const flo
   a.E = h->E;
   a.K = (int)h->K;
   a.N = (int)h->N;
-  a.C = C;
+  a.C = a.rows = C;
   a.n = nrows;
   a.xq = xq;
   a.xs = xs;
@@ -115,7 +115,7 @@ moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq, const flo
   a.limit_ns = 2000000000ull;   // 2 s per wait: far above any legitimate one
   a.num_sms = h->num_sms;
   a.st = static_cast<cudaStream_t>(stream);
-  return status_of(C <= 64 ? fp8_few(a) : fp8_matmul(a));
+  return status_of(fp8_matmul(a));
 }
 
 }  // extern "C"

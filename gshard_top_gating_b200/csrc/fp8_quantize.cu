@@ -8,6 +8,7 @@
 // zeros gets q = 0 and the scale 2^-100 / 448.  A block with a NaN becomes all NaN; one with
 // an infinity gets s = inf, whose products are NaN or infinite as well.
 #include "common.cuh"
+#include "glu.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -101,6 +102,48 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* __restri
   }
 }
 
+// The rows that experts hold: block (x, e) takes blocks of 128 of expert e's rows in turn.
+// FN >= 0: the values are h = f(g) * u of [g | u], formed in 32 bits and quantised from there.
+template <int FN>
+__global__ void __launch_bounds__(256) quantize_held_kernel(const void* __restrict__ x, uint2* __restrict__ q,
+                                                            float* __restrict__ s, const int32_t* __restrict__ nexp,
+                                                            int64_t C, uint32_t KB, int K) {
+  pdl_wait();
+  const int e = blockIdx.y;
+  const uint32_t lane = threadIdx.x & 15, mask = 0xFFFFu << (threadIdx.x & 16);
+  const int64_t nblocks = min(max((int64_t)nexp[e], (int64_t)0), C) * KB;
+  for (int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; b < nblocks; b += (int64_t)gridDim.x * 16) {
+    const int64_t row = (int64_t)e * C + b / KB;
+    const int k = (int)(b % KB) * 128 + (int)lane * 8;
+    float v[8] = {};
+    if (k < K) {
+      Raw8<true> raw;
+      if (FN < 0) {
+        raw.load(x, row * K + k);
+        raw.get(v);
+      } else {
+        float u[8];
+        raw.load(x, row * 2 * K + k);
+        raw.get(v);
+        raw.load(x, row * 2 * K + K + k);
+        raw.get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = glu_f<FN < 0 ? 0 : FN, true>(v[j]) * u[j];
+      }
+    }
+    float a = kTiny;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = amax2(a, v[j]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = amax2(a, __shfl_xor_sync(mask, a, o));
+    const float r = __fdiv_rn(kMax, a);
+    if (k < K)
+      q[(row * K + k) / 8] =
+          make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+    if (lane == 0) s[row * KB + (int)(b % KB)] = __fdiv_rn(a, kMax);
+  }
+}
+
 // One 128 x 128 tile of W[e] ([K, N]) per block of 256 threads, written transposed.
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* __restrict__ W, uint8_t* __restrict__ q,
@@ -167,6 +210,32 @@ cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* 
   if (K % 128 == 0)
     return bf16 ? launch_rows<true, true>(nblocks, KB, K, x, q, s, st) : launch_rows<false, true>(nblocks, KB, K, x, q, s, st);
   return bf16 ? launch_rows<true, false>(nblocks, KB, K, x, q, s, st) : launch_rows<false, false>(nblocks, KB, K, x, q, s, st);
+}
+
+namespace {
+
+template <int FN>
+cudaError_t launch_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s, cudaStream_t st) {
+  const uint32_t KB = (uint32_t)((K + 127) / 128);
+  // about eight blocks of threads per SM over all experts, and no more than an expert can use
+  int64_t per = (C * KB + 15) / 16, want = (148 * 8 + E - 1) / E;
+  if (want > per) want = per;
+  return launch_pdl(quantize_held_kernel<FN>, dim3((unsigned)want, E), dim3(256), 0, st, x, static_cast<uint2*>(q), s, n, C,
+                    KB, K);
+}
+
+}  // namespace
+
+cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s,
+                              cudaStream_t st) {
+  return launch_held<-1>(E, C, K, n, x, q, s, st);
+}
+
+cudaError_t fp8_quantize_glu(int E, int64_t C, int K, int fn, const int32_t* n, const void* gu, void* q, float* s,
+                             cudaStream_t st) {
+  if (fn == kGluSilu) return launch_held<kGluSilu>(E, C, K, n, gu, q, s, st);
+  if (fn == kGluGelu) return launch_held<kGluGelu>(E, C, K, n, gu, q, s, st);
+  return launch_held<kGluRelu>(E, C, K, n, gu, q, s, st);
 }
 
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st) {

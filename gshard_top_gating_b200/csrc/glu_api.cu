@@ -27,6 +27,9 @@ struct moe_glu {
   void* tx;              // [E, 64, M] act (bf16)
   void* tdy;
   int64_t saved_C;       // C of the last forward that kept g and u, or -1
+  // A forward was captured into a CUDA graph without keeping g and u: a replay of that graph,
+  // which the host cannot see, leaves those of another forward behind.
+  bool graph_without_gu;
 };
 
 namespace {
@@ -39,7 +42,7 @@ GluArgs args_of(moe_glu_handle h, int64_t C, const void* x, const int32_t* n, cu
   a.M = (int)h->M;
   a.H = (int)h->H;
   a.fn = h->fn;
-  a.C = C;
+  a.C = a.rows = C;
   a.Cp = h->Cp;
   a.n = n;
   a.x = x;
@@ -171,19 +174,12 @@ moe_status moe_glu_forward(moe_glu_handle h, int64_t C, const void* x, const int
   if (C > 0 && (!x || !y || !nrows || !is_aligned(x, 16) || !is_aligned(y, 16) || !is_aligned(nrows, 4)))
     return MOE_ERR_INVALID_ARG;
   h->saved_C = -1;
+  if (!h->bws && is_capturing(static_cast<cudaStream_t>(stream))) h->graph_without_gu = true;
   if (C > 0) {
     GluArgs a = args_of(h, C, x, nrows, static_cast<cudaStream_t>(stream));
     a.y = y;
-    if (h->act == MOE_BF16 && C <= 128) {
-      GLU_TRY(glu_few_up(a));
-      GLU_TRY(glu_few_down(a));
-    } else if (h->act == MOE_BF16) {
-      GLU_TRY(glu_up_bf16(a));
-      GLU_TRY(glu_down_bf16(a));
-    } else {
-      GLU_TRY(glu_up_f32(a));
-      GLU_TRY(glu_down_f32(a));
-    }
+    GLU_TRY(glu_up(a, h->act == MOE_BF16));
+    GLU_TRY(glu_down(a, h->act == MOE_BF16));
   }
   if (h->bws) h->saved_C = C;
   return MOE_OK;
@@ -193,7 +189,7 @@ moe_status moe_glu_backward(moe_glu_handle h, int64_t C, const void* x, const in
                             void* dW13, void* dW2, uint32_t flags, void* stream) {
   if (!h || C < 0 || C > h->C_max || !on_device(h->device) || (flags & ~(uint32_t)MOE_BWD_SKIP_EMPTY_EXPERTS))
     return MOE_ERR_INVALID_ARG;
-  if (!h->bws || h->saved_C != C) return MOE_ERR_STATE;
+  if (!h->bws || h->saved_C != C || h->graph_without_gu) return MOE_ERR_STATE;
   if (!dW13 || !dW2 || !is_aligned(dW13, 16) || !is_aligned(dW2, 16)) return MOE_ERR_INVALID_ARG;
   if (C > 0 && (!x || !dy || !dx || !nrows || !is_aligned(x, 16) || !is_aligned(dy, 16) || !is_aligned(dx, 16) ||
                 !is_aligned(nrows, 4)))

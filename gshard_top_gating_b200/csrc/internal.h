@@ -268,6 +268,7 @@ enum { kGluSilu = 0, kGluGelu = 1, kGluRelu = 2 };
 struct GluArgs {
   int E, M, H, fn;
   int64_t C;             // rows per expert of x, y, dy, dx
+  int64_t rows;          // most rows an expert may hold (<= C): which kernels run goes by it
   int64_t Cp;            // rows per expert of h, gu, dgu (a multiple of 256, >= C)
   const int32_t* n;      // [E] device: rows each expert holds, read as min(max(n, 0), C)
   const void* x;         // [E, C, M]
@@ -291,8 +292,10 @@ struct GluArgs {
   int num_sms;
   cudaStream_t st;
 };
-cudaError_t glu_up_bf16(const GluArgs& a);      // h (and gu)
-cudaError_t glu_down_bf16(const GluArgs& a);    // y
+cudaError_t glu_up(const GluArgs& a, bool bf16);      // h (and gu)
+cudaError_t glu_down(const GluArgs& a, bool bf16);    // y
+cudaError_t glu_up_bf16(const GluArgs& a);
+cudaError_t glu_down_bf16(const GluArgs& a);
 cudaError_t glu_tail_bf16(const GluArgs& a);    // tx, tdy
 cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu
 cudaError_t glu_dx_bf16(const GluArgs& a);      // dx
@@ -308,6 +311,7 @@ cudaError_t glu_dw13_f32(const GluArgs& a);
 struct Fp8Args {
   int E, K, N;
   int64_t C;             // rows per expert of xq, xs, y
+  int64_t rows;          // most rows an expert may hold (<= C): which kernel runs goes by it
   const int32_t* n;      // [E] device: rows each expert holds, read as min(max(n, 0), C)
   const void* xq;        // [E, C, K] e4m3
   const float* xs;       // [E, C, ceil(K/128)]
@@ -321,7 +325,8 @@ struct Fp8Args {
   int num_sms;
   cudaStream_t st;
 };
-cudaError_t fp8_matmul(const Fp8Args& a);
+cudaError_t fp8_matmul(const Fp8Args& a);       // few_rows.cu or 256 x 256 tiles
+cudaError_t fp8_pair(const Fp8Args& a);         // 256 x 256 tiles
 // few_rows.cu: the same products (gated experts' up and down in bf16, the 8-bit one) for few
 // rows.  Workspace: floats of partial sums (returned) and counts, zero before the first
 // launch; every launch leaves the counts zero.
@@ -331,6 +336,12 @@ cudaError_t glu_few_down(const GluArgs& a);
 cudaError_t fp8_few(const Fp8Args& a);
 // fp8_quantize.cu
 cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* q, float* s, cudaStream_t st);
+// The rows each expert holds of x [E, C, K] bf16 (n as in Fp8Args); and the same of
+// h = f(g) * u, [g | u] = gu [E, C, 2K] bf16.
+cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s,
+                              cudaStream_t st);
+cudaError_t fp8_quantize_glu(int E, int64_t C, int K, int fn, const int32_t* n, const void* gu, void* q, float* s,
+                             cudaStream_t st);
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st);
 // selftest.cu
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st);

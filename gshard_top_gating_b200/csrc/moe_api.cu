@@ -50,6 +50,21 @@ struct moe_layer {
   int host_slot;
   bool last_was_host;    // the handle's last device work was a moe_forward_host
   GemmPlan plan1, plan2;
+  // gated experts (moe_create_gated): W1 is [Wg | Wu], the expert kernels are glu_*
+  bool gated;
+  int fn;                // kGlu*
+  float* fpart;          // few_rows.cu: partial sums, arrival counts
+  unsigned* fcount;
+  size_t nfcount;
+  void* gu;              // training: [E, Cbuf, 2H] act, g and u (8-bit experts: every forward's)
+  // experts in 8 bits (moe_create_gated_fp8): e4m3 weights with their scales, quantised rows
+  bool fp8;
+  const float* W1s;
+  const float* W2s;
+  void* xq;              // [E, Cbuf, M] e4m3, scales [E, Cbuf, ceil(M/128)]
+  float* xs;
+  void* hq;              // [E, Cbuf, H] e4m3, scales [E, Cbuf, ceil(H/128)]
+  float* hs;
   void* wsplit;          // bf16 tokens: W_g split into three bf16 parts [3][EP][M]
   CUtensorMap wmap, xmap, xmap64;
   const void* xmap_ptr;  // x pointer / S the cached xmap describes
@@ -102,7 +117,7 @@ namespace {
 
 // Top-1 routing on an inference handle (no backward workspace): the second expert GEMM
 // stores its gate-scaled rows straight into y, and no combine kernel runs.
-bool fuses_combine(const moe_layer* h) { return h->slot_tok != nullptr && !h->bws; }
+bool fuses_combine(const moe_layer* h) { return h->slot_tok != nullptr && !h->bws && !h->gated; }
 
 // Forward expert GEMMs below capacity: CTA pairs for each expert's 256-row blocks and
 // one-CTA tiles for a last block of at most 128 rows (else 128-row tiles throughout).
@@ -156,21 +171,34 @@ size_t carve(moe_layer* h, char* base) {
   R.psum = c.take<float>(nchunk * E);
   R.lse2 = c.take<float>(nchunk);
   R.losses = c.take<float>(2);
-  R.err = c.take<unsigned>(1);
+  const size_t parts =
+      h->gated && h->act == MOE_BF16 ? few_rows_workspace(h->Cbuf, h->fp8, h->num_sms, &h->nfcount) : 0;
+  R.err = c.take<unsigned>(1 + h->nfcount);     // the error word, then the arrival counts
+  h->fcount = R.err ? R.err + 1 : nullptr;
   R.dest = c.take<int32_t>(S * k);
   R.alt = c.take<int32_t>(S * k);
   R.lrank2 = c.take<int32_t>(S * k);
   R.hist2 = c.take<int32_t>(k * nchunk * E);
   R.off2 = c.take<int32_t>(k * nchunk * E);
   h->xbuf = c.take<char>((size_t)E * h->Cbuf * h->M * as);
-  h->hbuf = c.take<char>((size_t)E * h->Cbuf * h->H * as);
+  const size_t rows = (size_t)E * h->Cbuf;
+  h->fpart = parts ? c.take<float>(parts) : nullptr;
+  if (h->fp8) {
+    h->xq = c.take<char>(rows * h->M);
+    h->xs = c.take<float>(rows * ((h->M + 127) / 128));
+    h->gu = c.take<char>(rows * 2 * h->H * as);
+    h->hq = c.take<char>(rows * h->H);
+    h->hs = c.take<float>(rows * ((h->H + 127) / 128));
+  } else {
+    h->hbuf = c.take<char>(rows * h->H * as);
+  }
   h->ybuf = c.take<char>((size_t)E * h->Cbuf * h->M * as);
   for (int b = 0; b < 2; ++b) {
     h->xstage[b] = c.take<char>((size_t)S * h->M * as);
     h->ystage[b] = c.take<char>((size_t)S * h->M * as);
   }
   h->wsplit = h->act == MOE_BF16 ? c.take<char>((size_t)3 * router_tc_pad(h->E) * h->M * 2) : nullptr;
-  const bool top1 = h->act == MOE_BF16 && k == 1;
+  const bool top1 = h->act == MOE_BF16 && k == 1 && !h->gated;
   h->slot_tok = top1 ? c.take<int32_t>((size_t)E * h->Cbuf) : nullptr;
   h->slot_gate = top1 ? c.take<float>((size_t)E * h->Cbuf) : nullptr;
   return c.off + 256;
@@ -182,7 +210,7 @@ moe_status read_device_error(moe_handle h, cudaStream_t st) {
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
   if (ce != cudaSuccess) return from_cuda(ce);
   if (e) {
-    cudaMemsetAsync(h->R.err, 0, sizeof(unsigned), st);
+    cudaMemsetAsync(h->R.err, 0, (1 + h->nfcount) * sizeof(unsigned), st);
     cudaStreamSynchronize(st);
     return (e & DEVERR_TIMEOUT) ? MOE_ERR_TIMEOUT : MOE_ERR_CUDA;
   }
@@ -194,6 +222,101 @@ moe_status read_device_error(moe_handle h, cudaStream_t st) {
     cudaError_t _e = (call);                     \
     if (_e != cudaSuccess) return from_cuda(_e); \
   } while (0)
+
+// Experts of a layer: ReLU, gated (fn >= 0), gated in 8 bits (with scales).
+struct Experts {
+  int fn;
+  const void* W1;
+  const void* W2;
+  const float* W1s;
+  const float* W2s;
+};
+
+moe_status create_layer(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
+                        double capacity_factor, moe_dtype act, const float* Wg, const float* bias,
+                        const Experts& ex) {
+  const void *W1 = ex.W1, *W2 = ex.W2;
+  if (!out) return MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (S_max < 1 || M < 64 || H < 64 || (M % 64) || (H % 64) || E < 1 || k < 1 || k > E)
+    return MOE_ERR_INVALID_ARG;
+  if (!(capacity_factor > 0.0) || !isfinite(capacity_factor)) return MOE_ERR_INVALID_ARG;
+  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!Wg || !W1 || !W2 || !aligned(Wg, 4) || !aligned(W1, 16) || !aligned(W2, 16) ||
+      (bias && !aligned(bias, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (ex.fn > kGluRelu || (ex.W1s && !aligned(ex.W1s, 4)) || (ex.W2s && !aligned(ex.W2s, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || k > kMaxK) return MOE_ERR_UNSUPPORTED;
+  if (S_max > (int64_t)1 << 30 || M > (1 << 16) || H > (1 << 16)) return MOE_ERR_UNSUPPORTED;
+
+  moe_layer* h = new (std::nothrow) moe_layer();
+  if (!h) return MOE_ERR_OOM;
+  h->S_max = S_max;
+  h->M = M;
+  h->H = H;
+  h->E = E;
+  h->k = k;
+  h->cf = capacity_factor;
+  h->act = act;
+  h->Wg = Wg;
+  h->bias = bias;
+  h->W1 = W1;
+  h->W2 = W2;
+  h->gated = ex.fn >= 0;
+  h->fn = ex.fn;
+  h->fp8 = ex.W1s != nullptr;
+  h->W1s = ex.W1s;
+  h->W2s = ex.W2s;
+  const int64_t C = capacity_of(capacity_factor, k, S_max, E);
+  // rows per expert: at most min(C, S_max) are kept; rounded up to 256 so every GEMM
+  // tile (128 rows, or 256 for a CTA pair) and its whole-tile stores stay inside the
+  // expert's own rows
+  const int64_t rows = C < S_max ? C : S_max;
+  h->Cbuf = (rows + 255) / 256 * 256;
+  // expert-buffer rows and token choices are 32-bit indices (TMA coordinates, tables)
+  if ((int64_t)E * h->Cbuf > INT32_MAX || S_max * k > INT32_MAX) {
+    delete h;
+    return MOE_ERR_UNSUPPORTED;
+  }
+  h->wait_limit_ns = 2000000000ull;   // 2 s per wait: far above any legitimate wait
+  cudaError_t ce = cudaGetDevice(&h->device);
+  if (ce == cudaSuccess)
+    ce = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+  if (ce != cudaSuccess) {
+    delete h;
+    return from_cuda(ce);
+  }
+  h->ws_bytes = carve(h, nullptr);
+  ce = cudaMalloc(&h->ws, h->ws_bytes);
+  if (ce != cudaSuccess) {
+    cudaGetLastError();
+    delete h;
+    return from_cuda(ce);
+  }
+  carve(h, static_cast<char*>(h->ws));
+  ce = cudaMemset(h->R.err, 0, (1 + h->nfcount) * sizeof(unsigned));
+  if (ce == cudaSuccess) ce = cudaMemset(h->R.losses, 0, 2 * sizeof(float));
+  if (ce != cudaSuccess) {
+    cudaFree(h->ws);
+    delete h;
+    return from_cuda(ce);
+  }
+  if (act == MOE_BF16) {
+    const bool ok1 = h->gated || make_gemm_plan(h->plan1, h->xbuf, W1, h->hbuf, E, h->Cbuf, (int)M, (int)H, true);
+    const bool ok2 = h->gated || make_gemm_plan(h->plan2, h->hbuf, W2, h->ybuf, E, h->Cbuf, (int)H, (int)M, false);
+    ce = split_gate_weights(Wg, (int)M, E, h->wsplit, 0);
+    if (ce == cudaSuccess) ce = cudaStreamSynchronize(0);
+    const bool ok3 = ce == cudaSuccess && make_router_wmap(&h->wmap, h->wsplit, (int)M, E);
+    if (!ok1 || !ok2 || !ok3) {
+      cudaFree(h->ws);
+      delete h;
+      return MOE_ERR_CUDA;
+    }
+  }
+  *out = h;
+  return MOE_OK;
+}
 
 }  // namespace
 
@@ -226,79 +349,25 @@ const char* moe_stage_name(int32_t s) {
 moe_status moe_create(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
                       double capacity_factor, moe_dtype act, const float* Wg, const float* bias,
                       const void* W1, const void* W2) {
+  return create_layer(out, S_max, M, H, E, k, capacity_factor, act, Wg, bias, Experts{-1, W1, W2, nullptr, nullptr});
+}
+
+moe_status moe_create_gated(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
+                            double capacity_factor, moe_dtype act, moe_glu_fn fn, const float* Wg,
+                            const float* bias, const void* W13, const void* W2) {
   if (!out) return MOE_ERR_INVALID_ARG;
   *out = nullptr;
-  if (S_max < 1 || M < 64 || H < 64 || (M % 64) || (H % 64) || E < 1 || k < 1 || k > E)
-    return MOE_ERR_INVALID_ARG;
-  if (!(capacity_factor > 0.0) || !isfinite(capacity_factor)) return MOE_ERR_INVALID_ARG;
-  if (act != MOE_F32 && act != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if (!Wg || !W1 || !W2 || !aligned(Wg, 4) || !aligned(W1, 16) || !aligned(W2, 16) ||
-      (bias && !aligned(bias, 4)))
-    return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || k > kMaxK) return MOE_ERR_UNSUPPORTED;
-  if (S_max > (int64_t)1 << 30 || M > (1 << 16) || H > (1 << 16)) return MOE_ERR_UNSUPPORTED;
+  if ((int)fn < 0) return MOE_ERR_INVALID_ARG;
+  return create_layer(out, S_max, M, H, E, k, capacity_factor, act, Wg, bias, Experts{(int)fn, W13, W2, nullptr, nullptr});
+}
 
-  moe_layer* h = new (std::nothrow) moe_layer();
-  if (!h) return MOE_ERR_OOM;
-  h->S_max = S_max;
-  h->M = M;
-  h->H = H;
-  h->E = E;
-  h->k = k;
-  h->cf = capacity_factor;
-  h->act = act;
-  h->Wg = Wg;
-  h->bias = bias;
-  h->W1 = W1;
-  h->W2 = W2;
-  const int64_t C = capacity_of(capacity_factor, k, S_max, E);
-  // rows per expert: at most min(C, S_max) are kept; rounded up to 256 so every GEMM
-  // tile (128 rows, or 256 for a CTA pair) and its whole-tile stores stay inside the
-  // expert's own rows
-  const int64_t rows = C < S_max ? C : S_max;
-  h->Cbuf = (rows + 255) / 256 * 256;
-  // expert-buffer rows and token choices are 32-bit indices (TMA coordinates, tables)
-  if ((int64_t)E * h->Cbuf > INT32_MAX || S_max * k > INT32_MAX) {
-    delete h;
-    return MOE_ERR_UNSUPPORTED;
-  }
-  h->wait_limit_ns = 2000000000ull;   // 2 s per wait: far above any legitimate wait
-  cudaError_t ce = cudaGetDevice(&h->device);
-  if (ce == cudaSuccess)
-    ce = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
-  if (ce != cudaSuccess) {
-    delete h;
-    return from_cuda(ce);
-  }
-  h->ws_bytes = carve(h, nullptr);
-  ce = cudaMalloc(&h->ws, h->ws_bytes);
-  if (ce != cudaSuccess) {
-    cudaGetLastError();
-    delete h;
-    return from_cuda(ce);
-  }
-  carve(h, static_cast<char*>(h->ws));
-  ce = cudaMemset(h->R.err, 0, sizeof(unsigned));
-  if (ce == cudaSuccess) ce = cudaMemset(h->R.losses, 0, 2 * sizeof(float));
-  if (ce != cudaSuccess) {
-    cudaFree(h->ws);
-    delete h;
-    return from_cuda(ce);
-  }
-  if (act == MOE_BF16) {
-    const bool ok1 = make_gemm_plan(h->plan1, h->xbuf, W1, h->hbuf, E, h->Cbuf, (int)M, (int)H, true);
-    const bool ok2 = make_gemm_plan(h->plan2, h->hbuf, W2, h->ybuf, E, h->Cbuf, (int)H, (int)M, false);
-    ce = split_gate_weights(Wg, (int)M, E, h->wsplit, 0);
-    if (ce == cudaSuccess) ce = cudaStreamSynchronize(0);
-    const bool ok3 = ce == cudaSuccess && make_router_wmap(&h->wmap, h->wsplit, (int)M, E);
-    if (!ok1 || !ok2 || !ok3) {
-      cudaFree(h->ws);
-      delete h;
-      return MOE_ERR_CUDA;
-    }
-  }
-  *out = h;
-  return MOE_OK;
+moe_status moe_create_gated_fp8(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
+                                double capacity_factor, moe_glu_fn fn, const float* Wg, const float* bias,
+                                const void* W13q, const float* W13s, const void* W2q, const float* W2s) {
+  if (!out) return MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if ((int)fn < 0 || !W13s || !W2s) return MOE_ERR_INVALID_ARG;
+  return create_layer(out, S_max, M, H, E, k, capacity_factor, MOE_BF16, Wg, bias, Experts{(int)fn, W13q, W2q, W13s, W2s});
 }
 
 moe_status moe_destroy(moe_handle h) {
@@ -332,8 +401,8 @@ moe_status moe_get_capacity(moe_handle h, int64_t S, int64_t* C_out) {
 int32_t moe_kernels_per_forward(moe_handle h, int64_t S) {
   if (!h || S <= 0) return 0;
   const bool reroute = (h->route_flags & MOE_ROUTE_REROUTE) != 0;
-  int n = reroute ? 8 : (fuses_combine(h) ? 5 : 6);
-  if (h->act == MOE_BF16 && kMixedTiles && h->Cbuf % 256 == 0) {
+  int n = (reroute ? 8 : (fuses_combine(h) ? 5 : 6)) + (h->fp8 ? 2 : 0);
+  if (h->act == MOE_BF16 && kMixedTiles && !h->gated && h->Cbuf % 256 == 0) {
     const int64_t C = capacity_of(h->cf, h->k, S, h->E);
     const bool saturated = (double)S * h->k / h->E >= (double)C;
     if (!saturated) n += (h->plan1.pair ? 1 : 0) + (h->plan2.pair ? 1 : 0);   // pair + rest launches
@@ -374,6 +443,60 @@ struct NvtxStages {
   }
 };
 
+// The gated experts' products on the layer's own buffers (padded with zeros to a multiple of
+// 64 rows where the backward reduces over them, so without tail copies).
+GluArgs glu_args(moe_handle h, int64_t S, cudaStream_t st) {
+  GluArgs a{};
+  a.E = h->E;
+  a.M = (int)h->M;
+  a.H = (int)h->H;
+  a.fn = h->fn;
+  a.C = a.Cp = h->Cbuf;
+  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
+  a.rows = C < S ? C : S;
+  a.n = h->R.nexp;
+  a.x = h->xbuf;
+  a.W13 = h->W1;
+  a.W2 = h->W2;
+  a.h = h->hbuf;
+  a.gu = h->bws ? h->gu : nullptr;
+  a.y = h->ybuf;
+  a.dy = h->dybuf;
+  a.dgu = h->dpre;
+  a.dx = h->dybuf;          // dY is no longer needed once dW2 and dh are known
+  a.part = h->fpart;
+  a.count = h->fcount;
+  a.err = h->R.err;
+  a.limit_ns = h->wait_limit_ns;
+  a.num_sms = h->num_sms;
+  a.st = st;
+  return a;
+}
+
+Fp8Args fp8_args(moe_handle h, int64_t S, cudaStream_t st, const void* xq, const float* xs, int K, const void* wq,
+                 const float* ws, int N, void* y) {
+  Fp8Args a{};
+  a.E = h->E;
+  a.K = K;
+  a.N = N;
+  a.C = h->Cbuf;
+  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
+  a.rows = C < S ? C : S;
+  a.n = h->R.nexp;
+  a.xq = xq;
+  a.xs = xs;
+  a.wq = wq;
+  a.ws = ws;
+  a.y = y;
+  a.part = h->fpart;
+  a.count = h->fcount;
+  a.err = h->R.err;
+  a.limit_ns = h->wait_limit_ns;
+  a.num_sms = h->num_sms;
+  a.st = st;
+  return a;
+}
+
 moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStream_t st) {
   if (!h || S < 0 || S > h->S_max) return MOE_ERR_INVALID_ARG;
   if (S > 0 && (!x || !y || !aligned(x, 16) || !aligned(y, 16))) return MOE_ERR_INVALID_ARG;
@@ -382,7 +505,7 @@ moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStr
   h->fwd_data = true;
   h->bits_valid = false;
   h->last_fused = false;
-  if (h->act == MOE_BF16 && !h->plan1.bits) {
+  if (h->gated ? !h->bws : h->act == MOE_BF16 && !h->plan1.bits) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     // an error (a capture elsewhere in global mode) counts as capturing
     if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone)
@@ -441,7 +564,19 @@ moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStr
   else
     MOE_TRY(launch_dispatch(x, bf16, iS, iM, h->E, h->k, C, h->Cbuf, R, h->xbuf, st));
   MOE_TRY(mark(3));
-  if (bf16) {
+  if (h->fp8) {
+    MOE_TRY(fp8_quantize_held(h->E, h->Cbuf, iM, R.nexp, h->xbuf, h->xq, h->xs, st));
+    MOE_TRY(fp8_matmul(fp8_args(h, S, st, h->xq, h->xs, iM, h->W1, h->W1s, 2 * iH, h->gu)));
+    MOE_TRY(mark(4));
+    MOE_TRY(fp8_quantize_glu(h->E, h->Cbuf, iH, h->fn, R.nexp, h->gu, h->hq, h->hs, st));
+    MOE_TRY(fp8_matmul(fp8_args(h, S, st, h->hq, h->hs, iH, h->W2, h->W2s, iM, h->ybuf)));
+  } else if (h->gated) {
+    const GluArgs a = glu_args(h, S, st);
+    MOE_TRY(glu_up(a, bf16));
+    h->bits_valid = h->bws != nullptr;       // g and u kept
+    MOE_TRY(mark(4));
+    MOE_TRY(glu_down(a, bf16));
+  } else if (bf16) {
     // CTA-pair GEMMs (256-row tiles) when the experts run at capacity, so the
     // rows per expert are close to C and the 256-row padding stays small;
     // otherwise 128-row tiles waste less on partly filled last tiles.
@@ -641,6 +776,7 @@ moe_status moe_get_expert_rows(moe_handle h, int32_t which, int32_t e, int64_t n
   h->last_was_host = false;
   if (!h->have_forward || !h->fwd_data) return MOE_ERR_STATE;
   if (which == MOE_BUF_Y && h->last_fused) return MOE_ERR_STATE;   // stored straight into y
+  if (which == MOE_BUF_H && h->fp8) return MOE_ERR_UNSUPPORTED;    // held in 8 bits
   if (nrows == 0) return MOE_OK;
   const size_t as = act_bytes(h->act);
   const int64_t width = which == MOE_BUF_H ? h->H : h->M;
@@ -673,6 +809,7 @@ moe_status moe_get_stage_times(moe_handle h, float* ms, int32_t n) {
 
 moe_status moe_enable_backward(moe_handle h) {
   if (!h) return MOE_ERR_INVALID_ARG;
+  if (h->fp8) return MOE_ERR_UNSUPPORTED;
   if (h->bws) return MOE_OK;
   const size_t as = act_bytes(h->act);
   const int64_t rowsE = (int64_t)h->E * h->Cbuf;
@@ -685,14 +822,15 @@ moe_status moe_enable_backward(moe_handle h) {
   for (int pass = 0; pass < 2; ++pass) {
     c.off = 0;
     h->dybuf = c.take<char>((size_t)rowsE * h->M * as);
-    h->dpre = c.take<char>((size_t)rowsE * h->H * as);
+    h->dpre = c.take<char>((size_t)rowsE * h->H * as * (h->gated ? 2 : 1));
+    h->gu = h->gated ? c.take<char>((size_t)rowsE * 2 * h->H * as) : nullptr;
     h->dl = bf16 ? nullptr : c.take<float>((size_t)h->S_max * h->E);
     h->dgate = c.take<float>((size_t)h->S_max * h->k);
     h->part = c.take<float>(h->part_floats);
     h->dlb = bf16 ? c.take<char>((size_t)h->S_max * 2 * h->EPb * 2) : nullptr;
     h->bpart = bf16 ? c.take<float>((size_t)4 * h->num_sms * h->E) : nullptr;
     h->cnt_rows = bf16 ? c.take<int32_t>((size_t)1 + ns_max) : nullptr;
-    h->hbits = bf16 ? c.take<uint32_t>((size_t)rowsE * (h->H / 32)) : nullptr;
+    h->hbits = bf16 && !h->gated ? c.take<uint32_t>((size_t)rowsE * (h->H / 32)) : nullptr;
     if (pass == 0) {
       const size_t bytes = c.off + 256;
       cudaError_t ce = cudaMalloc(&h->bws, bytes);
@@ -704,7 +842,8 @@ moe_status moe_enable_backward(moe_handle h) {
       c.base = static_cast<char*>(h->bws);
     }
   }
-  if (h->act == MOE_BF16) {
+  if (h->gated) h->bits_valid = false;      // the last forward kept neither g nor u
+  if (h->act == MOE_BF16 && !h->gated) {
     const int M = (int)h->M, H = (int)h->H;
     const bool ok = make_dgrad_plan(h->plan_dp, h->dybuf, h->W2, h->dpre, h->hbuf, h->E, h->Cbuf, M, H) &&
                     make_dgrad_plan(h->plan_dx, h->dpre, h->W1, h->dybuf, nullptr, h->E, h->Cbuf, H, M);
@@ -741,6 +880,8 @@ moe_status moe_backward(moe_handle h, int64_t S, const void* x, const void* dy, 
   h->last_was_host = false;
   if (!h->bws || !h->have_forward || !h->fwd_data || S != h->last_S) return MOE_ERR_STATE;
   if (h->last_fused) return MOE_ERR_STATE;            // that forward kept no expert outputs
+  // gated experts: that forward kept g and u, and no graph's replay can have run one that did not
+  if (h->gated && S > 0 && (!h->bits_valid || h->graph_without_bits)) return MOE_ERR_STATE;
   if (!dWg || !dW1 || !dW2 || !aligned(dWg, 16) || !aligned(dW1, 16) || !aligned(dW2, 16) ||
       (dbias && !aligned(dbias, 4)))
     return MOE_ERR_INVALID_ARG;
@@ -754,7 +895,7 @@ moe_status moe_backward(moe_handle h, int64_t S, const void* x, const void* dy, 
     MOE_TRY(cudaMemsetAsync(dWg, 0, (size_t)M * E * 4, st));
     if (dbias) MOE_TRY(cudaMemsetAsync(dbias, 0, (size_t)E * 4, st));
     if (!(h->bwd_flags & MOE_BWD_SKIP_EMPTY_EXPERTS)) {   // every expert is empty
-      MOE_TRY(cudaMemsetAsync(dW1, 0, (size_t)E * M * H * as, st));
+      MOE_TRY(cudaMemsetAsync(dW1, 0, (size_t)E * M * H * as * (h->gated ? 2 : 1), st));
       MOE_TRY(cudaMemsetAsync(dW2, 0, (size_t)E * H * M * as, st));
     }
     return MOE_OK;
@@ -818,7 +959,25 @@ moe_status moe_backward(moe_handle h, int64_t S, const void* x, const void* dy, 
   MOE_TRY(mark(0));
   MOE_TRY(launch_gate_backward(a, R, st));
   MOE_TRY(mark(1));
-  if (bf16) {
+  if (h->gated) {
+    GluArgs g = glu_args(h, S, st);
+    g.dW13 = dW1;
+    g.dW2 = dW2;
+    g.skip_empty = (h->bwd_flags & MOE_BWD_SKIP_EMPTY_EXPERTS) != 0;
+    if (bf16) {      // the weight gradients reduce over whole 64-slot blocks (h, dg and du end in zeros)
+      void* bufs[2] = {h->xbuf, h->dybuf};
+      const int widths[2] = {M, M};
+      MOE_TRY(launch_pad_zero(bufs, widths, 2, true, E, h->Cbuf, R, st));
+    }
+    MOE_TRY(mark(2));
+    MOE_TRY(bf16 ? glu_dw2_bf16(g) : glu_dw2_f32(g));
+    MOE_TRY(mark(3));
+    MOE_TRY(bf16 ? glu_dh_bf16(g) : glu_dh_f32(g));
+    MOE_TRY(mark(4));
+    MOE_TRY(bf16 ? glu_dw13_bf16(g) : glu_dw13_f32(g));
+    MOE_TRY(mark(5));
+    MOE_TRY(bf16 ? glu_dx_bf16(g) : glu_dx_f32(g));
+  } else if (bf16) {
     if (h->dw2_ptr != dW2) {
       if (!make_wgrad_plan(h->plan_dw2, h->hbuf, h->dybuf, dW2, E, h->Cbuf, H, M)) return MOE_ERR_CUDA;
       h->dw2_ptr = dW2;

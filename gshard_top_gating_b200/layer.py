@@ -5,6 +5,9 @@
     l_aux, z = layer.aux_loss()                                  # moe_aux_loss
     g = layer.backward(x, dy, a_aux, a_z)                        # moe_backward
 
+Gated experts (activation "silu", "gelu" or "relu"): W1 is [Wg | Wu], [E, M, 2H].  With W1
+and W2 the pairs (q, s) of fp8.quantize_weights, the experts are held in 8 bits (inference).
+
 The tensors passed in are borrowed by the C library; this object keeps Python
 references to them so they outlive the handle.
 """
@@ -13,11 +16,29 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .experts import ACTIVATIONS, check_tensor
 
 
 class MoeLayer:
-    def __init__(self, S_max, M, H, E, k, capacity_factor, Wg, gate_bias, W1, W2):
-        act = W1.dtype
+    def __init__(self, S_max, M, H, E, k, capacity_factor, Wg, gate_bias, W1, W2, activation=None):
+        fp8 = isinstance(W1, tuple)
+        if fp8 != isinstance(W2, tuple):
+            raise TypeError("W1 and W2 are both pairs (q, s) of quantised weights, or neither is")
+        if activation is not None and activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, or None for ReLU experts")
+        if fp8:
+            if activation is None:
+                raise ValueError("experts in 8 bits are gated: give an activation")
+            (W1, W1s), (W2, W2s) = W1, W2
+            nb = lambda n: (n + 127) // 128  # noqa: E731
+            for name, t, shape, dt in (("W1", W1, (E, 2 * H, M), torch.float8_e4m3fn), ("W2", W2, (E, M, H), torch.float8_e4m3fn),
+                                       ("W1's scales", W1s, (E, nb(2 * H), nb(M)), torch.float32),
+                                       ("W2's scales", W2s, (E, nb(M), nb(H)), torch.float32)):
+                check_tensor(name, t, shape, dt, Wg.device)
+        elif activation is not None:
+            check_tensor("W1", W1, (E, M, 2 * H), W1.dtype, Wg.device)
+            check_tensor("W2", W2, (E, H, M), W1.dtype, Wg.device)
+        act = torch.bfloat16 if fp8 else W1.dtype
         if act not in (torch.float32, torch.bfloat16):
             raise TypeError("expert weights must be float32 or bfloat16")
         for t in (Wg, W1, W2) + ((gate_bias,) if gate_bias is not None else ()):
@@ -29,7 +50,16 @@ class MoeLayer:
         self.cf = capacity_factor
         self.act = act
         self._keep = (Wg, gate_bias, W1, W2)
-        self.h = L.moe_create(S_max, M, H, E, k, capacity_factor, act, Wg, gate_bias, W1, W2)
+        self.W1_cols = H if activation is None else 2 * H
+        if fp8:
+            self._keep += (W1s, W2s)
+            self.h = L.moe_create_gated_fp8(S_max, M, H, E, k, capacity_factor, ACTIVATIONS[activation], Wg, gate_bias, W1,
+                                            W1s, W2, W2s)
+        elif activation is not None:
+            self.h = L.moe_create_gated(S_max, M, H, E, k, capacity_factor, act, ACTIVATIONS[activation], Wg, gate_bias,
+                                        W1, W2)
+        else:
+            self.h = L.moe_create(S_max, M, H, E, k, capacity_factor, act, Wg, gate_bias, W1, W2)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if x.dtype != self.act or not x.is_contiguous() or x.dim() != 2 or x.shape[1] != self.M:
@@ -78,7 +108,7 @@ class MoeLayer:
             dbias = out.get("dbias") if out.get("dbias") is not None else \
                 torch.empty(self.E, dtype=torch.float32, device=dev)
         dW1 = out.get("dW1") if out.get("dW1") is not None else \
-            torch.empty(self.E, self.M, self.H, dtype=self.act, device=dev)
+            torch.empty(self.E, self.M, self.W1_cols, dtype=self.act, device=dev)
         dW2 = out.get("dW2") if out.get("dW2") is not None else \
             torch.empty(self.E, self.H, self.M, dtype=self.act, device=dev)
         for t in (dx, dWg, dW1, dW2) + ((dbias,) if dbias is not None else ()):

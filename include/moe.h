@@ -97,6 +97,40 @@ MOE_API moe_status moe_create(moe_handle* out, int64_t S_max, int64_t M, int64_t
                       double capacity_factor, moe_dtype act, const float* Wg_dev,
                       const float* gate_bias_dev, const void* W1_dev, const void* W2_dev);
 
+/* The gate function f of gated experts. */
+typedef enum {
+  MOE_GLU_SILU = 0,      /* f(g) = g / (1 + e^-g) */
+  MOE_GLU_GELU = 1,      /* f(g) = g (1 + erf(g / sqrt 2)) / 2 */
+  MOE_GLU_RELU = 2       /* f(g) = max(g, 0), f'(0) = 0 */
+} moe_glu_fn;
+
+/*
+ * moe_create_gated -- a layer with gated experts, ybuf = h W2[e] with h = f(xbuf Wg[e]) * (xbuf
+ * Wu[e]) in place of the ReLU network (the products of moe_glu_*, below).  As moe_create,
+ * with fn one of moe_glu_fn and W13_dev [E, M, 2H] act = [Wg | Wu] (Wg in columns 0 .. H-1).
+ * All calls on the handle work as for a ReLU layer: MOE_BUF_H holds h; moe_backward writes
+ * dW1 as [E, M, 2H] and returns MOE_ERR_STATE for a forward that ran before
+ * moe_enable_backward (which kept neither g nor u; so too once such a forward has been
+ * captured into a CUDA graph).  Top-1 routing keeps its combine kernel.
+ */
+MOE_API moe_status moe_create_gated(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
+                                    double capacity_factor, moe_dtype act, moe_glu_fn fn, const float* Wg_dev,
+                                    const float* gate_bias_dev, const void* W13_dev, const void* W2_dev);
+
+/*
+ * moe_create_gated_fp8 -- the same layer for inference with experts in 8 bits (the products and
+ * quantisers of moe_fp8_*, below): x and y are bf16, the dispatched rows and h are quantised
+ * per 1 x 128 block before each product, g and u are rounded to bf16 between.  The weights
+ * are what moe_fp8_quantize_weights makes of W13 and W2: W13q_dev [E, 2H, M] e4m3 with
+ * W13s_dev [E, ceil(2H/128), ceil(M/128)], W2q_dev [E, M, H] with W2s_dev [E, ceil(M/128),
+ * ceil(H/128)].  moe_enable_backward, and moe_get_expert_rows of MOE_BUF_H, return
+ * MOE_ERR_UNSUPPORTED.
+ */
+MOE_API moe_status moe_create_gated_fp8(moe_handle* out, int64_t S_max, int64_t M, int64_t H, int32_t E, int32_t k,
+                                        double capacity_factor, moe_glu_fn fn, const float* Wg_dev,
+                                        const float* gate_bias_dev, const void* W13q_dev, const float* W13s_dev,
+                                        const void* W2q_dev, const float* W2s_dev);
+
 /*
  * moe_forward -- one layer forward of S tokens (0 <= S <= S_max), enqueued on `stream`.
  *
@@ -557,12 +591,6 @@ MOE_API const char* moe_backward_stage_name(int32_t stage);
  */
 typedef struct moe_glu* moe_glu_handle;
 
-typedef enum {
-  MOE_GLU_SILU = 0,      /* f(g) = g / (1 + e^-g) */
-  MOE_GLU_GELU = 1,      /* f(g) = g (1 + erf(g / sqrt 2)) / 2 */
-  MOE_GLU_RELU = 2       /* f(g) = max(g, 0), f'(0) = 0 */
-} moe_glu_fn;
-
 /*
  * moe_glu_create -- handle of E gated experts (1 .. 256) for up to C_max rows each
  * (1 .. 2^21; E * round256(C_max) below 2^31, else MOE_ERR_UNSUPPORTED).  M, H: multiples
@@ -592,7 +620,8 @@ MOE_API moe_status moe_glu_enable_backward(moe_glu_handle h);
  * and dW2_dev [E, H, M] overwritten, all act, 16-byte aligned, none overlapping another or
  * an input.  An expert without rows gets zero weight gradients, or with
  * MOE_BWD_SKIP_EMPTY_EXPERTS in `flags` none.  MOE_ERR_STATE unless that forward came after
- * moe_glu_enable_backward.
+ * moe_glu_enable_backward, and once a forward before it has been captured into a CUDA graph
+ * (whose replays the host cannot see).
  */
 MOE_API moe_status moe_glu_backward(moe_glu_handle h, int64_t C, const void* x_dev, const int32_t* nrows_dev,
                                     const void* dy_dev, void* dx_dev, void* dW13_dev, void* dW2_dev,

@@ -200,3 +200,19 @@ def test_fp8_calls_are_rejected_before_device_work(L):
     assert L.lib.moe_fp8_quantize_rows(0, 32, 1, None, None, None, None) == 0
     assert L.lib.moe_fp8_quantize_weights(1, 32, 12, 1, FAKE, FAKE, FAKE, None) == 1
     assert L.lib.moe_fp8_quantize_weights(0, 32, 16, 1, FAKE, FAKE, FAKE, None) == 1
+
+
+def test_gated_layers_reject_bad_arguments_before_device_work(L):
+    h = ctypes.c_void_p(123)
+    good = (64, 64, 64, 8, 2, 1.0)
+    for args, act, fn, status in ((good, 1, 3, 1), (good, 1, -1, 1), (good, 2, 0, 1), ((64, 96, 64, 8, 2, 1.0), 1, 0, 1),
+                                  ((64, 64, 64, 300, 2, 1.0), 1, 0, 2)):
+        assert L.lib.moe_create_gated(ctypes.byref(h), *args, act, fn, FAKE, None, FAKE, FAKE) == status
+        assert h.value is None
+    for fn, ptrs, status in ((3, (FAKE,) * 4, 1), (0, (FAKE, None, FAKE, FAKE), 1), (0, (FAKE, FAKE, FAKE, None), 1),
+                             (0, (None, FAKE, FAKE, FAKE), 1), (0, (FAKE + 8, FAKE, FAKE, FAKE), 1),
+                             (0, (FAKE, FAKE + 2, FAKE, FAKE), 1)):
+        assert L.lib.moe_create_gated_fp8(ctypes.byref(h), *good, fn, FAKE, None, *ptrs) == status
+        assert h.value is None
+    assert L.lib.moe_create_gated(None, *good, 1, 0, FAKE, None, FAKE, FAKE) == 1
+    assert L.lib.moe_create_gated_fp8(None, *good, 0, FAKE, None, FAKE, FAKE, FAKE, FAKE) == 1

@@ -1,0 +1,303 @@
+"""The layer with gated experts, in bf16, fp32 and 8 bits, against its formulas in 64 bits (GPU).
+
+The layer's own routing (ids, gates, slots) is read back and held fixed, as in the ReLU
+layer's tests; its routing itself is checked against the oracle given the same logits.
+Outputs and gradients are held to the ReLU layer's bars: max |d| / max |ref| 2e-2 (bf16) and
+1e-4 (fp32) for y, and in relative Frobenius norm 1e-2 and 1e-3 for the gradients.
+
+Experts in 8 bits: a value is off by at most half a step of e4m3, 2^-4 of itself, spread
+evenly below that: 2^-4 / sqrt(3) = 0.0361 in norm for a tensor, sqrt(2) times that, 0.0511,
+for a product of two.  g and u carry it, h = f(g) u at most (1.13 + 1) / sqrt(2) times it if
+their errors are independent, 0.0769; its own rounding and W2's join: sqrt(0.0769^2 + 2 *
+0.0361^2) = 0.0924, and with the roundings to bf16 (2^-8 each, three) 0.093.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gshard_top_gating_b200 import _lib as L
+from gshard_top_gating_b200.inputs import Workload, make_inputs, upstream_grad
+from gshard_top_gating_b200.layer import MoeLayer
+
+pytestmark = pytest.mark.gpu
+
+TOL_Y = {torch.float32: 1e-4, torch.bfloat16: 2e-2}
+TOL_G = {torch.float32: 1e-3, torch.bfloat16: 1e-2}
+
+
+def gate_fn(name, g):
+    if name == "silu":
+        return g * torch.sigmoid(g)
+    return g * torch.special.ndtr(g) if name == "gelu" else g.clamp(min=0)
+
+
+def build(S, M, H, E, k, cf, act, fn, S_max=None, seed=0, bias=False):
+    w = Workload("case", S, M, H, E, k, cf, act, skew_bias=bias, seed=seed)
+    x, Wg, b, W1, W2 = make_inputs(w, device="cuda")
+    # [Wg | Wu]: two independent weights of the ReLU layer's first one
+    W13 = torch.cat([W1, make_inputs(w.with_(seed=seed + 1), device="cuda")[3]], 2).contiguous()
+    layer = MoeLayer(S_max or S, M, H, E, k, cf, Wg, b, W13, W2, activation=fn)
+    return w, x, Wg, b, W13, W2, layer
+
+
+def reference(x, Wg, b, W13, W2, fn, ids, slot, dy=None, a_aux=0.0, a_z=0.0):
+    """The layer in 64 bits with the routing (ids and drops) given; gradients by autograd."""
+    leaves = [t.double().requires_grad_(dy is not None) for t in (x, Wg, W13, W2)] + \
+        ([b.double().requires_grad_(dy is not None)] if b is not None else [])
+    X, G, A, B = leaves[:4]
+    S, E, H = x.shape[0], Wg.shape[1], W2.shape[1]
+    logits = X @ G + (leaves[4] if b is not None else 0.0)
+    p = torch.softmax(logits, 1)
+    gates = torch.gather(p, 1, ids)
+    gates = gates / gates.sum(1, keepdim=True)
+    parts = torch.zeros(S, x.shape[1], dtype=torch.float64, device=x.device)
+    for r in range(ids.shape[1]):
+        for e in range(E):
+            t = torch.nonzero((ids[:, r] == e) & (slot[:, r] >= 0))[:, 0]
+            if t.numel():
+                gu = X[t] @ A[e]
+                parts = parts.index_add(0, t, gates[t, r:r + 1] * ((gate_fn(fn, gu[:, :H]) * gu[:, H:]) @ B[e]))
+    if dy is None:
+        return parts
+    f = torch.bincount(ids[:, 0], minlength=E).double() / S
+    loss = (parts * dy.double()).sum() + a_aux * E * (f * p.mean(0)).sum() + a_z * (torch.logsumexp(logits, 1) ** 2).mean()
+    g = torch.autograd.grad(loss, leaves)
+    return parts.detach(), dict(zip(("dx", "dWg", "dW1", "dW2", "dbias"), g))
+
+
+def routing(layer, S, k, cf):
+    eidx, gate, slot, cnt = layer.routing(S)
+    rt = O.route(layer.logits(S).cpu().numpy(), k, cf)
+    assert np.array_equal(eidx.cpu().numpy(), rt.ids) and np.array_equal(slot.cpu().numpy(), rt.slot)
+    return eidx.long(), slot
+
+
+def relmax(got, ref):
+    return float((got.double() - ref).abs().max() / ref.abs().max().clamp(min=1e-300))
+
+
+def relnorm(got, ref):
+    return float((got.double() - ref).norm() / ref.norm().clamp(min=1e-300))
+
+
+SHAPES = [
+    # S, M, H, E, k, cf, act
+    (256, 64, 256, 8, 2, 1.25, "f32"),
+    (100, 128, 192, 4, 2, 1.0, "f32"),
+    (300, 256, 512, 8, 2, 1.25, "bf16"),
+    (257, 192, 320, 6, 2, 1.0, "bf16"),
+    (1000, 128, 256, 8, 1, 1.0, "bf16"),       # top-1
+    (2000, 128, 192, 4, 2, 0.5, "bf16"),       # at capacity, many rows: CTA-pair tiles
+    (1500, 320, 448, 2, 2, 2.0, "bf16"),
+    (400, 64, 64, 32, 4, 1.5, "bf16"),
+    (1, 128, 256, 8, 2, 1.25, "bf16"),         # one token
+]
+
+
+@pytest.mark.parametrize("fn", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_forward_and_backward(shape, fn):
+    S, M, H, E, k, cf, act = shape
+    w, x, Wg, b, W13, W2, layer = build(*shape, fn, bias=S == 257)
+    y0 = layer(x)                                  # inference: before enable_backward
+    layer.enable_backward()
+    y = layer(x)
+    l_aux, z = layer.aux_loss()
+    ids, slot = routing(layer, S, k, cf)
+    dy = upstream_grad(w, device="cuda")
+    g = layer.backward(x, dy, 0.5, 0.1)
+    assert g["dW1"].shape == (E, M, 2 * H)
+    ref, gr = reference(x, Wg, b, W13, W2, fn, ids, slot, dy, 0.5, 0.1)
+    assert relmax(y, ref) <= TOL_Y[x.dtype] and relmax(y0, ref) <= TOL_Y[x.dtype]
+    for name, want in gr.items():
+        if name == "dWg" and (k == E or E == 1):
+            continue
+        assert relnorm(g[name], want) <= TOL_G[x.dtype], (name, relnorm(g[name], want))
+    layer.close()
+
+
+def test_experts_are_the_operator_on_the_dispatched_rows():
+    """MOE_BUF_X through GatedExperts gives MOE_BUF_Y bit for bit, and h is f(g) u of them."""
+    from gshard_top_gating_b200.experts import GatedExperts
+    S, M, H, E, k, cf = 1200, 128, 256, 4, 2, 1.25
+    w, x, Wg, b, W13, W2, layer = build(S, M, H, E, k, cf, "bf16", "silu")
+    layer(x)
+    C = layer.capacity(S)
+    n = layer.routing(S)[3].clamp(max=C)
+    rows = torch.stack([layer.expert_rows(L.MOE_BUF_X, e, C) for e in range(E)])
+    want = torch.stack([layer.expert_rows(L.MOE_BUF_Y, e, C) for e in range(E)])
+    got = GatedExperts(C, W13, W2)(rows, n)
+    for e in range(E):
+        r = int(n[e])
+        assert torch.equal(got[e, :r], want[e, :r])
+        gu = rows[e, :r].double() @ W13[e].double()
+        h = torch.nn.functional.silu(gu[:, :H]) * gu[:, H:]
+        assert relnorm(layer.expert_rows(L.MOE_BUF_H, e, r), h) <= 2.0**-8
+
+
+def test_short_batches_on_a_long_layer_and_rerouting():
+    w, x, Wg, b, W13, W2, layer = build(600, 128, 256, 8, 2, 1.0, "bf16", "silu", S_max=4096, seed=3)
+    for S in (1, 3, 64, 600):
+        xs = x[:S].contiguous()
+        y = layer(xs)
+        ids, slot = routing(layer, S, 2, 1.0)
+        assert relmax(y, reference(xs, Wg, b, W13, W2, "silu", ids, slot)) <= 2e-2
+    assert layer(x[:0].contiguous()).shape == (0, 128)
+    layer.set_rerouting(True)
+    y = layer(x)
+    dest, slot = layer.serving_experts(600).long(), layer.routing(600)[2]
+    gates = layer.routing(600)[1].double()
+    out = torch.zeros(600, 128, dtype=torch.float64, device="cuda")
+    for r in range(2):
+        for e in range(8):
+            t = torch.nonzero((dest[:, r] == e) & (slot[:, r] >= 0))[:, 0]
+            gu = x[t].double() @ W13[e].double()
+            out.index_add_(0, t, gates[t, r:r + 1] * ((gate_fn("silu", gu[:, :256]) * gu[:, 256:]) @ W2[e].double()))
+    assert relmax(y, out) <= 2e-2
+
+
+def test_captured_training_step():
+    w, x, Wg, b, W13, W2, layer = build(500, 128, 256, 4, 2, 1.25, "bf16", "silu")
+    layer.enable_backward()
+    dy = upstream_grad(w, device="cuda")
+    y = torch.empty_like(x)
+    layer(x, out=y)
+    want = layer.backward(x, dy, 0.1, 0.01)
+    out = {n: torch.zeros_like(t) for n, t in want.items() if t is not None}
+    y2 = torch.zeros_like(y)
+    layer(x, out=y2)
+    layer.backward(x, dy, 0.1, 0.01, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(x, out=y2)
+        layer.backward(x, dy, 0.1, 0.01, out=out)
+    for t in out.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2)
+    for name, t in out.items():
+        assert torch.equal(t, want[name]), name
+
+
+def test_backward_needs_a_forward_that_kept_g_and_u():
+    w, x, Wg, b, W13, W2, layer = build(200, 64, 128, 4, 2, 1.25, "bf16", "silu")
+    dy = upstream_grad(w, device="cuda")
+    layer(x)
+    with pytest.raises(L.MoeError) as err:
+        layer.backward(x, dy)
+    assert err.value.status == L.MOE_ERR_STATE
+    layer(x)
+    layer.backward(x, dy)
+    # once a forward without them has been captured, its replays cannot be told apart
+    w, x, Wg, b, W13, W2, other = build(200, 64, 128, 4, 2, 1.25, "bf16", "silu")
+    y = torch.empty_like(x)
+    other(x, out=y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other(x, out=y)
+    other.enable_backward()
+    other(x)
+    with pytest.raises(L.MoeError) as err:
+        other.backward(x, dy)
+    assert err.value.status == L.MOE_ERR_STATE
+
+
+def test_kernels_per_call_and_refusals():
+    w, x, Wg, b, W13, W2, layer = build(64, 64, 128, 4, 1, 1.25, "bf16", "silu")
+    assert L.moe_kernels_per_forward(layer.h, 64) == 6 and L.moe_kernels_per_backward(layer.h, 64) == 10
+    for bad in ("tanh", "SILU", 3):
+        with pytest.raises(ValueError):
+            MoeLayer(64, 64, 128, 4, 1, 1.25, Wg, b, W13, W2, activation=bad)
+    with pytest.raises(ValueError):
+        MoeLayer(64, 64, 128, 4, 1, 1.25, Wg, b, W13[:, :, :128].contiguous(), W2, activation="silu")
+
+
+# ------------------------------------------------------------------ experts in 8 bits
+
+def build8(S, M, H, E, k, cf, fn, S_max=None, seed=0):
+    from gshard_top_gating_b200.fp8 import quantize_weights
+    w, x, Wg, b, W13, W2, exact = build(S, M, H, E, k, cf, "bf16", fn, S_max=S_max, seed=seed)
+    layer = MoeLayer(S_max or S, M, H, E, k, cf, Wg, b, quantize_weights(W13), quantize_weights(W2), activation=fn)
+    return x, Wg, b, W13, W2, exact, layer
+
+
+@pytest.mark.parametrize("fn", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("shape", [(300, 256, 512, 8, 2, 1.25), (257, 192, 320, 6, 2, 1.0), (1500, 320, 448, 2, 2, 2.0),
+                                   (1, 128, 256, 8, 2, 1.25), (900, 128, 64, 4, 1, 0.5)], ids=lambda s: "x".join(map(str, s)))
+def test_layer_in_8_bits(shape, fn):
+    S, M, H, E, k, cf = shape
+    x, Wg, b, W13, W2, exact, layer = build8(*shape, fn)
+    y = layer(x)
+    L.moe_check(layer.h)
+    ids, slot = routing(layer, S, k, cf)
+    ref = reference(x, Wg, b, W13, W2, fn, ids, slot)
+    assert relnorm(y, ref) <= 0.093, relnorm(y, ref)
+    assert torch.equal(layer(x), y)
+    dropped = (slot < 0).all(1)
+    assert not y[dropped].any()
+    assert L.moe_kernels_per_forward(layer.h, S) == 8
+
+
+def test_layer_in_8_bits_is_its_operators_in_turn():
+    """The dispatched rows through quantize_rows, Fp8Matmul, f(g) u and again: what differs is
+    f evaluated another way (2^-20), which moves few values of h across a rounding to e4m3."""
+    from gshard_top_gating_b200.fp8 import Fp8Matmul, quantize_rows, quantize_weights
+    S, M, H, E, k, cf = 1200, 256, 384, 4, 2, 1.25
+    x, Wg, b, W13, W2, exact, layer = build8(S, M, H, E, k, cf, "silu")
+    layer(x)
+    C = layer.capacity(S)
+    n = layer.routing(S)[3].clamp(max=C)
+    rows = torch.stack([layer.expert_rows(L.MOE_BUF_X, e, C) for e in range(E)])
+    want = torch.stack([layer.expert_rows(L.MOE_BUF_Y, e, C) for e in range(E)])
+    live = torch.arange(C, device="cuda")[None, :, None] < n[:, None, None]
+    rows = torch.where(live, rows, torch.zeros_like(rows))
+    up, down = Fp8Matmul(C, *quantize_weights(W13)), Fp8Matmul(C, *quantize_weights(W2))
+    gu = up(*quantize_rows(rows), n, out=torch.zeros(E, C, 2 * H, dtype=torch.bfloat16, device="cuda")).float()
+    h = torch.nn.functional.silu(gu[:, :, :H]) * gu[:, :, H:]
+    y = down(*quantize_rows(h), n, out=torch.zeros_like(rows))
+    for e in range(E):
+        r = int(n[e])
+        assert relnorm(want[e, :r], y[e, :r].double()) <= 2.0**-8
+
+
+def test_short_batches_and_capture_in_8_bits():
+    x, Wg, b, W13, W2, exact, layer = build8(400, 128, 256, 8, 2, 1.25, "silu", S_max=2048, seed=5)
+    for S in (1, 2, 64, 400):
+        xs = x[:S].contiguous()
+        y = layer(xs)
+        ids, slot = routing(layer, S, 2, 1.25)
+        assert relnorm(y, reference(xs, Wg, b, W13, W2, "silu", ids, slot)) <= 0.093
+    want = layer(x)
+    y = torch.empty_like(x)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        layer(x, out=y)
+    y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_refusals_in_8_bits():
+    x, Wg, b, W13, W2, exact, layer = build8(64, 64, 128, 4, 2, 1.25, "silu")
+    layer(x)
+    with pytest.raises(L.MoeError) as err:
+        layer.enable_backward()
+    assert err.value.status == L.MOE_ERR_UNSUPPORTED
+    with pytest.raises(L.MoeError) as err:
+        layer.expert_rows(L.MOE_BUF_H, 0, 1)
+    assert err.value.status == L.MOE_ERR_UNSUPPORTED
+    from gshard_top_gating_b200.fp8 import quantize_weights
+    q1, q2 = quantize_weights(W13), quantize_weights(W2)
+    for args, act in (((q1, W2), "silu"), ((q1, q2), None), ((q2, q1), "silu"), (((q1[0], q1[1][:, :, :0]), q2), "silu")):
+        with pytest.raises((TypeError, ValueError)):
+            MoeLayer(64, 64, 128, 4, 2, 1.25, Wg, b, *args, activation=act)
