@@ -775,9 +775,8 @@ cudaError_t launch_nt(int nt, const CUtensorMap& tmW, const CUtensorMap& tmX, co
   switch (nt) {
     case 16: return launch<KIND, 16, FN>(tmW, tmX, f, num_sms, st);
     case 32: return launch<KIND, 32, FN>(tmW, tmX, f, num_sms, st);
-    case 64: return launch<KIND, 64, FN>(tmW, tmX, f, num_sms, st);
   }
-  if constexpr (KIND != kFp8) return launch<KIND, 128, FN>(tmW, tmX, f, num_sms, st);
+  if constexpr (KIND == kFp8) return launch<KIND, 64, FN>(tmW, tmX, f, num_sms, st);
   else return cudaErrorInvalidValue;
 }
 
@@ -788,7 +787,7 @@ int row_tile(int64_t C, int most) {
   return nt;
 }
 
-constexpr int kMostBf16 = 128, kMostFp8 = 64;
+constexpr int kMostBf16 = 32, kMostFp8 = 64;
 
 }  // namespace
 
@@ -875,17 +874,38 @@ cudaError_t fp8_few(const Fp8Args& a) {
   return launch_nt<kFp8, kGluSilu>(nt, tmW, tmX, f, a.num_sms, a.st);
 }
 
+// When this file's kernels run (us, all experts full; here : 256 x 256 tiles).  They win while
+// the weights' stream hides the joining of parts, whose cost grows with the rows, and where
+// there are too few 256 x 256 tiles for the device.
+//   gated experts, E x M x H, rows 16 / 32 / 64:
+//     1 x 1024 x 4096    28 : 36    37 : 36    53 : 36
+//     1 x 2048 x 8192    48 : 87    60 : 88    86 : 89
+//     8 x 1024 x 4096    55 : 57    65 : 57    79 : 58
+//     32 x 1024 x 4096  152 : 159  176 : 162  184 : 168
+//   8-bit product, E x K x N, rows 16 / 32 / 64 / 128:
+//     1 x 1456 x 2008    11 : 13    14 : 13    17 : 13    18 : 14
+//     1 x 7168 x 4096    16 : 40    23 : 39    31 : 40    35 : 42
+//     8 x 7168 x 4096    52 : 80    67 : 78    89 : 82   161 : 85
+//     32 x 2048 x 7168   86 : 158  106 : 155  213 : 161  406 : 168
+bool glu_few(const GluArgs& a) {
+  return a.rows <= 16 || (a.rows <= kMostBf16 && (int64_t)a.E * ((a.M + 255) / 256) <= 8);
+}
+
+bool fp8_few_wins(const Fp8Args& a) {
+  return a.rows <= 32 || (a.rows <= 128 && a.K >= 4096 && (int64_t)a.E * ((a.N + 255) / 256) <= 16);
+}
+
 // Both sides run both products of the gated experts alike, so that `down` finds `up` before it.
 cudaError_t glu_up(const GluArgs& a, bool bf16) {
   if (!bf16) return glu_up_f32(a);
-  return a.rows <= kMostBf16 ? glu_few_up(a) : glu_up_bf16(a);
+  return glu_few(a) ? glu_few_up(a) : glu_up_bf16(a);
 }
 
 cudaError_t glu_down(const GluArgs& a, bool bf16) {
   if (!bf16) return glu_down_f32(a);
-  return a.rows <= kMostBf16 ? glu_few_down(a) : glu_down_bf16(a);
+  return glu_few(a) ? glu_few_down(a) : glu_down_bf16(a);
 }
 
-cudaError_t fp8_matmul(const Fp8Args& a) { return a.rows <= kMostFp8 ? fp8_few(a) : fp8_pair(a); }
+cudaError_t fp8_matmul(const Fp8Args& a) { return fp8_few_wins(a) ? fp8_few(a) : fp8_pair(a); }
 
 }  // namespace moe

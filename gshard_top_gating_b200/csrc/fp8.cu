@@ -28,8 +28,8 @@ constexpr int BK = 128;                 // depth of a stage = of a scale block (
 constexpr int PM = 256, PN = 256;
 constexpr int kThreads = 384;           // loads, MMAs and two idle warps; eight draining warps
 constexpr int kDrainWarps = 8;
-// Registers: 384 threads launch with 168 each (64,512); 128 keep 72, 256 take 216 (the same).
-constexpr int kRegsLoad = 72, kRegsDrain = 216;
+// Registers: 384 threads launch with 168 each (64,512); 128 keep 40, 256 take 232 (the same).
+constexpr int kRegsLoad = 40, kRegsDrain = 232;
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 5;
 constexpr uint32_t TMEM_COLS = 2 * PN;
@@ -219,55 +219,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool live = lane < nvalid && nb < a.NB;
       const float* xs = a.xs + (row0 + (live ? lane : 0)) * KB;
       const float* ws = a.ws + ((int64_t)e * a.NB + (live ? nb : 0)) * KB;
-      float sum[128];
+      uint64_t sum[64];                          // 128 columns, two per register pair
 #pragma unroll
-      for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+      for (int j = 0; j < 64; ++j) sum[j] = 0ull;
       auto scale = [&](int kb, float& x, float& w) {
         x = live && kb < KB ? __ldg(xs + kb) : 0.f;
         w = live && kb < KB ? __ldg(ws + kb) : 0.f;
       };
-      // adds block kb; its scales were loaded two blocks ago, those of block kb + 2 are now
+      // adds block kb; its scales were loaded four blocks ago, those of block kb + 4 are now
       auto drain = [&](int kb, float& x, float& w) -> bool {
         if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
           *abort_flag = 1;
           return false;
         }
         tc_fence_after();
-        const float sc = x * w;
-        scale(kb + 2, x, w);
+        const float f = x * w;
+        const uint64_t sc = pack_f32x2(f, f);
+        scale(kb + 4, x, w);
         const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + half * 128;
-        uint32_t r[2][32];
-        if (nvalid > 0) tmem_ld_32x32b_x32(tm, r[0]);
+        // two groups of 32 columns in flight; the last two are on their way while the first two
+        // are added, and the buffer is handed back before those are added
+        uint32_t r0[32], r1[32];
+        auto add = [&](int c, const uint32_t (&r)[32]) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (nvalid > 0) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld_32x32b_x32(tm + (c + 1) * 32, r[(c + 1) & 1]);
-          }
-          if (c == 3) {                   // the buffer's last column is here: hand it back
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (leader) mbar_arrive(tempty_bar(acc));
-              else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
-            }
-          }
-          if (nvalid > 0) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[c * 32 + j] = fmaf(sc, __uint_as_float(r[c & 1][j]), sum[c * 32 + j]);
-          }
+          for (int j = 0; j < 16; ++j)         // two columns per instruction
+            sum[c * 16 + j] = fma_f32x2(sc, pack_u32x2(r[2 * j], r[2 * j + 1]), sum[c * 16 + j]);
+        };
+        tmem_ld_32x32b_x32(tm, r0);            // (rows past the last one: garbage times 0, not stored)
+        tmem_ld_32x32b_x32(tm + 32, r1);
+        tmem_ld_wait();
+        add(0, r0);
+        tmem_ld_32x32b_x32(tm + 64, r0);
+        add(1, r1);
+        tmem_ld_32x32b_x32(tm + 96, r1);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(tempty_bar(acc));
+          else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
         }
+        add(2, r0);
+        add(3, r1);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
         return true;
       };
-      float x0, w0, x1, w1;
-      scale(0, x0, w0);
-      scale(1, x1, w1);
-      for (int kb = 0; ok && kb < KB; kb += 2) {
-        ok = drain(kb, x0, w0);
-        if (ok && kb + 1 < KB) ok = drain(kb + 1, x1, w1);
-      }
+      float x[4], w[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) scale(d, x[d], w[d]);
+      for (int kb = 0; ok && kb < KB; kb += 4)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          if (ok && kb + d < KB) ok = drain(kb + d, x[d], w[d]);
       if (ok && nvalid > 0) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -281,7 +285,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) {
               uint32_t pk[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(sum[b * 64 + j * 8 + 2 * i], sum[b * 64 + j * 8 + 2 * i + 1]);
+              for (int i = 0; i < 4; ++i) {
+                const uint64_t v = sum[b * 32 + j * 4 + i];
+                pk[i] = pack_bf16x2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+              }
               if (nvalid == 32)
                 st_shared_v4(tile0 + lane * 128 + ((j ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
               else if (lane < nvalid && col + j * 8 < a.N)       // N is a multiple of 8
