@@ -46,9 +46,7 @@ constexpr int kJoin = 4;                    // parts on their way to the joining
 
 template <int KIND, int NT>
 struct Few {
-  // accumulators: g and u of 128 features, or two times 128 features (64 rows of an 8-bit
-  // product: one, its sums are kept in registers)
-  static constexpr int ACC = KIND == kFp8 && NT > 32 ? 1 : 2;
+  static constexpr int ACC = 2;                                 // accumulators: g and u, or two times 128 features
   static constexpr int FEATURES = KIND == kUp ? 128 : 128 * ACC;   // of a tile
   static constexpr uint32_t STAGE = ACC * A_BYTES + NT * 128;
   static constexpr int FIT = (int)((220 * 1024) / STAGE);
@@ -56,7 +54,6 @@ struct Few {
   static constexpr int BUFS = KIND == kFp8 ? 4 : 2;             // accumulator buffers in TMEM
   static constexpr int COLS = BUFS * ACC * NT;
   static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr bool FETCH = NT <= 32;                       // (wider tiles: the parts would take too much memory)
   static constexpr uint32_t kBars = 512;
   static constexpr uint32_t kMisc = 256;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + kBars + kMisc + 4 * (3 * kMaxExperts + 1);
@@ -271,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Cuts c{};
       c.T = c.Ts = inc;
       c.P = 1;
-      if (F::FETCH && (long long)inc * KB >= (long long)kLongShare * grid) {
+      if ((long long)inc * KB >= (long long)kLongShare * grid) {
         const int td = min(inc / 5, kPieces * grid);
         if (td > 0) {
           c.Ts = inc - td;
@@ -376,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++t;
         kb = 0;
       }
-      if (F::FETCH && npieces > 0) {
+      if (npieces > 0) {
         unsigned* next = a.count + (1 + kPieces) * grid;
         int id = ok ? (int)atomicAdd(next, 1u) : npieces;
         for (int r = 0;; ++r) {
@@ -461,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++t;
         kb = 0;
       }
-      if (F::FETCH && npieces > 0)
+      if (npieces > 0)
         for (int r = 0; ok; ++r) {
           const int slot = r % kRing;
           if (*abort_flag || !mbar_wait(pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
@@ -521,58 +518,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < NT; ++k) sum[j][k] = 0.f;
         const float* ws = a.ws + ((int64_t)t.e * a.NB + t.nt * ACC) * KB;
-        const bool second = ACC == 2 && t.nt * ACC + 1 < a.NB;      // the tile has a second block of 128
+        const bool second = t.nt * ACC + 1 < a.NB;      // the tile has a second block of 128
         const float* xs = a.xs + (t.e * a.Cb + row0) * KB;
-        constexpr int XR = (NT + 31) / 32;     // lane l holds the scales of rows l, l + 32, ...
         constexpr int AHEAD = 4;               // blocks whose scales are on their way
-        float x[AHEAD][XR], w[AHEAD][ACC];
-        auto scales = [&](int i, float (&xv)[XR], float (&wv)[ACC]) {
+        float x[AHEAD], w[AHEAD][ACC];         // lane l holds the scale of row l
+        auto scales = [&](int i, float& xv, float (&wv)[ACC]) {
           const int kb = st.kb + i;
           wv[0] = i < st.len ? __ldg(ws + kb) : 0.f;
-          if (ACC == 2) wv[ACC - 1] = i < st.len && second ? __ldg(ws + KB + kb) : 0.f;
-#pragma unroll
-          for (int r = 0; r < XR; ++r)
-            xv[r] = i < st.len && r * 32 + lane < nvalid ? __ldg(xs + (int64_t)(r * 32 + lane) * KB + kb) : 0.f;
+          wv[1] = i < st.len && second ? __ldg(ws + KB + kb) : 0.f;
+          xv = i < st.len && lane < nvalid ? __ldg(xs + (int64_t)lane * KB + kb) : 0.f;
         };
-        auto drain = [&](int i, float (&xv)[XR], float (&wv)[ACC]) {
+        auto drain = [&](int i, float& xv, float (&wv)[ACC]) {
           if (*abort_flag || !mbar_wait(tfull_bar(buf), bph, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
             return;
           }
           tc_fence_after();
-          float sx[XR], sw[ACC];
-#pragma unroll
-          for (int r = 0; r < XR; ++r) sx[r] = xv[r];
-#pragma unroll
-          for (int j = 0; j < ACC; ++j) sw[j] = wv[j];
+          const float sx = xv, sw[ACC] = {wv[0], wv[1]};
           scales(i + AHEAD, xv, wv);
-          constexpr int AT_ONCE = ACC == 2 ? 1 : 2;       // 16-column groups in registers
 #pragma unroll
-          for (int k0 = 0; k0 < NT / 16; k0 += AT_ONCE) {
-          uint32_t v[ACC][AT_ONCE][16];
+          for (int k = 0; k < NT; k += 16) {
+            uint32_t v[ACC][16];
+            if (k < nvalid) {
 #pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k)
-            if ((k0 + k) * 16 < nvalid) {
-#pragma unroll
-              for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm0 + buf * (ACC * NT) + j * NT + (k0 + k) * 16, v[j][k]);
+              for (int j = 0; j < ACC; ++j) tmem_ld_32x32b_x16(tm0 + buf * (ACC * NT) + j * NT + k, v[j]);
             }
-          tmem_ld_wait();
-          if (k0 + AT_ONCE == NT / 16) {       // the last columns are here: hand the buffer back
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(buf));
-          }
-#pragma unroll
-          for (int k = 0; k < AT_ONCE; ++k)
-            if ((k0 + k) * 16 < nvalid) {
+            tmem_ld_wait();
+            if (k + 16 == NT) {                // the last columns are here: hand the buffer back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tempty_bar(buf));
+            }
+            if (k < nvalid) {
 #pragma unroll
               for (int i2 = 0; i2 < 16; ++i2) {
-                const int col = (k0 + k) * 16 + i2;
-                const float s = __shfl_sync(0xffffffffu, sx[col / 32], col % 32);
+                const float s = __shfl_sync(0xffffffffu, sx, k + i2);
 #pragma unroll
                 for (int j = 0; j < ACC; ++j)
-                  sum[j][col] = fmaf(s * sw[j], __uint_as_float(v[j][k][i2]), sum[j][col]);
+                  sum[j][k + i2] = fmaf(s * sw[j], __uint_as_float(v[j][i2]), sum[j][k + i2]);
               }
             }
           }
@@ -648,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++t;
       kb = 0;
     }
-    if (F::FETCH && npieces > 0)
+    if (npieces > 0)
       for (int r = 0; ok; ++r) {
         const int slot = r % kRing;
         if (*abort_flag || !mbar_wait(pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
@@ -770,41 +754,19 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const FewArgs
   return launch_pdl(kern, dim3(num_sms), dim3(kThreads), smem, st, tmW, tmX, f);
 }
 
-template <int KIND, int FN>
-cudaError_t launch_nt(int nt, const CUtensorMap& tmW, const CUtensorMap& tmX, const FewArgs& f, int num_sms, cudaStream_t st) {
-  switch (nt) {
-    case 16: return launch<KIND, 16, FN>(tmW, tmX, f, num_sms, st);
-    case 32: return launch<KIND, 32, FN>(tmW, tmX, f, num_sms, st);
-  }
-  if constexpr (KIND == kFp8) return launch<KIND, 64, FN>(tmW, tmX, f, num_sms, st);
-  else return cudaErrorInvalidValue;
-}
-
-// Rows per tile: the smallest that holds C.
-int row_tile(int64_t C, int most) {
-  int nt = 16;
-  while (nt < C && nt < most) nt *= 2;
-  return nt;
-}
-
-constexpr int kMostBf16 = 32, kMostFp8 = 64;
+constexpr int kRowsBf16 = 16, kRowsFp8 = 32;     // most rows an expert may hold, and the widest tile
 
 }  // namespace
 
-size_t few_rows_workspace(int64_t C_max, bool fp8, int num_sms, size_t* counts) {
-  const int nt = row_tile(C_max, fp8 ? kMostFp8 : kMostBf16);
+size_t few_rows_workspace(bool fp8, int num_sms, size_t* counts) {
   *counts = (size_t)(1 + kPieces) * num_sms + 2;
-  // the widest tile takes most, the fetched pieces of tiles of up to 32 rows included
-  const size_t lane = (size_t)num_sms * 2 * 128;
-  const size_t shares = 2 * lane * nt, pieces = (2 + kPieces) * lane * (nt < 32 ? nt : 32);
-  return shares > pieces ? shares : pieces;
+  return (size_t)(2 + kPieces) * num_sms * 2 * (fp8 ? kRowsFp8 : kRowsBf16) * 128;
 }
 
 cudaError_t glu_few_up(const GluArgs& a) {
-  const int nt = row_tile(a.rows, kMostBf16);
   CUtensorMap tmW, tmX;
   if (!encode_column_blocks(&tmW, a.W13, 2 * (uint64_t)a.H, (uint64_t)a.E * a.M, 2) ||
-      !encode_2d(&tmX, a.x, a.M, (uint64_t)a.E * a.C, 64, nt))
+      !encode_2d(&tmX, a.x, a.M, (uint64_t)a.E * a.C, 64, kRowsBf16))
     return cudaErrorInvalidValue;
   FewArgs f{};
   f.n = a.n;
@@ -821,16 +783,15 @@ cudaError_t glu_few_up(const GluArgs& a) {
   f.count = a.count;
   f.err = a.err;
   f.limit_ns = a.limit_ns;
-  if (a.fn == kGluSilu) return launch_nt<kUp, kGluSilu>(nt, tmW, tmX, f, a.num_sms, a.st);
-  if (a.fn == kGluGelu) return launch_nt<kUp, kGluGelu>(nt, tmW, tmX, f, a.num_sms, a.st);
-  return launch_nt<kUp, kGluRelu>(nt, tmW, tmX, f, a.num_sms, a.st);
+  if (a.fn == kGluSilu) return launch<kUp, kRowsBf16, kGluSilu>(tmW, tmX, f, a.num_sms, a.st);
+  if (a.fn == kGluGelu) return launch<kUp, kRowsBf16, kGluGelu>(tmW, tmX, f, a.num_sms, a.st);
+  return launch<kUp, kRowsBf16, kGluRelu>(tmW, tmX, f, a.num_sms, a.st);
 }
 
 cudaError_t glu_few_down(const GluArgs& a) {
-  const int nt = row_tile(a.rows, kMostBf16);
   CUtensorMap tmW, tmX;
   if (!encode_column_blocks(&tmW, a.W2, a.M, (uint64_t)a.E * a.H, 4) ||
-      !encode_2d(&tmX, a.h, a.H, (uint64_t)a.E * a.Cp, 64, nt))
+      !encode_2d(&tmX, a.h, a.H, (uint64_t)a.E * a.Cp, 64, kRowsBf16))
     return cudaErrorInvalidValue;
   FewArgs f{};
   f.n = a.n;
@@ -846,13 +807,13 @@ cudaError_t glu_few_down(const GluArgs& a) {
   f.count = a.count;
   f.err = a.err;
   f.limit_ns = a.limit_ns;
-  return launch_nt<kDown, kGluSilu>(nt, tmW, tmX, f, a.num_sms, a.st);
+  return launch<kDown, kRowsBf16, kGluSilu>(tmW, tmX, f, a.num_sms, a.st);
 }
 
 cudaError_t fp8_few(const Fp8Args& a) {
-  const int nt = row_tile(a.rows, kMostFp8);
+  const int nt = a.rows <= 16 ? 16 : 32;
   CUtensorMap tmW, tmX;
-  if (!encode_2d_bytes(&tmW, a.wq, a.K, (uint64_t)a.E * a.N, 128, nt <= 32 ? 256 : 128) ||
+  if (!encode_2d_bytes(&tmW, a.wq, a.K, (uint64_t)a.E * a.N, 128, 256) ||
       !encode_2d_bytes(&tmX, a.xq, a.K, (uint64_t)a.E * a.C, 128, nt))
     return cudaErrorInvalidValue;
   FewArgs f{};
@@ -871,28 +832,24 @@ cudaError_t fp8_few(const Fp8Args& a) {
   f.count = a.count;
   f.err = a.err;
   f.limit_ns = a.limit_ns;
-  return launch_nt<kFp8, kGluSilu>(nt, tmW, tmX, f, a.num_sms, a.st);
+  return nt == 16 ? launch<kFp8, 16, kGluSilu>(tmW, tmX, f, a.num_sms, a.st) : launch<kFp8, 32, kGluSilu>(tmW, tmX, f, a.num_sms, a.st);
 }
 
-// When this file's kernels run (us, all experts full; here : 256 x 256 tiles).  They win while
-// the weights' stream hides the joining of parts, whose cost grows with the rows, and where
-// there are too few 256 x 256 tiles for the device.
-//   gated experts, E x M x H, rows 16 / 32 / 64:
-//     1 x 1024 x 4096    28 : 36    37 : 36    53 : 36
-//     1 x 2048 x 8192    48 : 87    60 : 88    86 : 89
-//     8 x 1024 x 4096    55 : 57    65 : 57    79 : 58
-//     32 x 1024 x 4096  152 : 159  176 : 162  184 : 168
-//   8-bit product, E x K x N, rows 16 / 32 / 64 / 128:
-//     1 x 1456 x 2008    11 : 13    14 : 13    17 : 13    18 : 14
-//     1 x 7168 x 4096    16 : 40    23 : 39    31 : 40    35 : 42
-//     8 x 7168 x 4096    52 : 80    67 : 78    89 : 82   161 : 85
-//     32 x 2048 x 7168   86 : 158  106 : 155  213 : 161  406 : 168
+// When this file's kernels run (us, all experts full; here : 256 x 256 tiles).  The joining of
+// parts grows with the rows, so few rows win, and in bf16, where tiles come near the memory's
+// rate too, with 9 to 16 rows only many weights.
+//   gated experts, E x M x H, rows 1 / 8 / 16 / 32:
+//     1 x 1024 x 4096    19 : 24    22 : 23    27 : 23    37 : 23
+//     1 x 2048 x 8192    29 : 45    33 : 42    41 : 44    53 : 40
+//     8 x 1024 x 4096    47 : 60    50 : 51    54 : 53    66 : 52
+//     32 x 1024 x 4096  135 : 168  142 : 162  155 : 165  178 : 168
+//   8-bit product, E x K x N, rows 1 / 16 / 32 / 64:
+//     1 x 1456 x 2008    10 : 11    11 : 13    14 : 13    17 : 13
+//     1 x 7168 x 4096    12 : 18    16 : 24    23 : 23    30 : 25
+//     8 x 7168 x 4096    48 : 68    53 : 69    67 : 67    88 : 70
+//     32 x 2048 x 7168   80 : 131   87 : 137  106 : 136  213 : 142
 bool glu_few(const GluArgs& a) {
-  return a.rows <= 16 || (a.rows <= kMostBf16 && (int64_t)a.E * ((a.M + 255) / 256) <= 8);
-}
-
-bool fp8_few_wins(const Fp8Args& a) {
-  return a.rows <= 32 || (a.rows <= 128 && a.K >= 4096 && (int64_t)a.E * ((a.N + 255) / 256) <= 16);
+  return a.rows <= 8 || (a.rows <= kRowsBf16 && (int64_t)a.E * a.M * a.H >= (1 << 24));
 }
 
 // Both sides run both products of the gated experts alike, so that `down` finds `up` before it.
@@ -906,6 +863,6 @@ cudaError_t glu_down(const GluArgs& a, bool bf16) {
   return glu_few(a) ? glu_few_down(a) : glu_down_bf16(a);
 }
 
-cudaError_t fp8_matmul(const Fp8Args& a) { return fp8_few_wins(a) ? fp8_few(a) : fp8_pair(a); }
+cudaError_t fp8_matmul(const Fp8Args& a) { return a.rows <= kRowsFp8 ? fp8_few(a) : fp8_pair(a); }
 
 }  // namespace moe

@@ -32,6 +32,7 @@ constexpr int kDrainWarps = 8;
 constexpr int kRegsLoad = 40, kRegsDrain = 232;
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 5;
+constexpr double kBlockUs = 0.6;        // 256 x 256 x 128 on a pair, drained
 constexpr uint32_t TMEM_COLS = 2 * PN;
 constexpr uint32_t TILE_BYTES = 4096;   // 32 rows x 64 bf16 columns
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;
@@ -43,13 +44,17 @@ static_assert(SMEM + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
 struct Fp8Pair {
   const int32_t* n;
   int E, C, K, N, KB, NB;
+  int n_max;             // counts are read as min(max(n, 0), n_max)
   const float* xs;       // [E, C, KB]
   const float* ws;       // [E, NB, KB]
   __nv_bfloat16* y;
+  int splits, rows;      // shares of a tile's depth (split.cu); most rows an expert holds
+  float* part;           // splits > 1: [splits][E, rows, N] fp32 sums instead of y
   unsigned* err;
   uint64_t limit_ns;
 };
 
+template <bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const Fp8Pair a) {
@@ -76,7 +81,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int NT = (a.N + PN - 1) / PN;
-  const int KB = a.KB;
+  const int KB = a.KB, splits = SPLIT ? a.splits : 1;
+  // item -> tile, and the item's blocks of depth
+  auto tile_of = [&](int item) { return SPLIT ? item / splits : item; };
+  auto depth_of = [&](int item, int& from, int& to) {
+    const int s = SPLIT ? item % splits : 0;
+    from = SPLIT ? KB * s / splits : 0;
+    to = SPLIT ? KB * (s + 1) / splits : KB;
+    return s;
+  };
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -104,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int e0 = lane * per;
     int sum = 0;
     for (int e = e0; e < min(a.E, e0 + per); ++e) {
-      nrows[e] = min(max(a.n[e], 0), a.C);
+      nrows[e] = min(max(a.n[e], 0), a.n_max);
       mtiles[e] = (nrows[e] + PM - 1) / PM;
       sum += mtiles[e] * NT;
     }
@@ -136,10 +149,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       int e, mt, nt;
-      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+      for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs) {
         const int rowA = e * a.C + mt * PM + (int)rank * 128;
         const int rowB = e * a.N + nt * PN + (int)rank * 128;
-        for (int kb = 0; kb < KB; ++kb) {
+        int from, to;
+        depth_of(tile, from, to);
+        for (int kb = from; kb < to; ++kb) {
           if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
@@ -169,8 +184,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       int e, mt, nt;
-      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
-        for (int kb = 0; kb < KB; ++kb) {
+      for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs) {
+        int from, to;
+        depth_of(tile, from, to);
+        for (int kb = from; kb < to; ++kb) {
           if (*abort_flag || !mbar_wait(tempty_bar(acc), aph ^ 1u, a.err, a.limit_ns) ||
               !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
             *abort_flag = 1;
@@ -210,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int e, mt, nt, acc = 0;
     uint32_t aph = 0;
     bool ok = true;
-    for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+    for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs) {
       const int local = mt * PM + (int)rank * 128 + q * 32;
       const int nvalid = min(32, nrows[e] - local);
       const int64_t row0 = (int64_t)e * a.C + local;
@@ -219,12 +236,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool live = lane < nvalid && nb < a.NB;
       const float* xs = a.xs + (row0 + (live ? lane : 0)) * KB;
       const float* ws = a.ws + ((int64_t)e * a.NB + (live ? nb : 0)) * KB;
+      int from, to;
+      depth_of(tile, from, to);
       uint64_t sum[64];                          // 128 columns, two per register pair
 #pragma unroll
       for (int j = 0; j < 64; ++j) sum[j] = 0ull;
       auto scale = [&](int kb, float& x, float& w) {
-        x = live && kb < KB ? __ldg(xs + kb) : 0.f;
-        w = live && kb < KB ? __ldg(ws + kb) : 0.f;
+        x = live && kb < to ? __ldg(xs + kb) : 0.f;
+        w = live && kb < to ? __ldg(ws + kb) : 0.f;
       };
       // adds block kb; its scales were loaded four blocks ago, those of block kb + 4 are now
       auto drain = [&](int kb, float& x, float& w) -> bool {
@@ -267,12 +286,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       float x[4], w[4];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) scale(d, x[d], w[d]);
-      for (int kb = 0; ok && kb < KB; kb += 4)
+      for (int d = 0; d < 4; ++d) scale(from + d, x[d], w[d]);
+      for (int kb = from; ok && kb < to; kb += 4)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          if (ok && kb + d < KB) ok = drain(kb + d, x[d], w[d]);
-      if (ok && nvalid > 0) {
+          if (ok && kb + d < to) ok = drain(kb + d, x[d], w[d]);
+      if (SPLIT) {
+        if (ok && lane < nvalid) {
+          float* p = a.part + (((int64_t)depth_of(tile, from, to) * a.E + e) * a.rows + local + lane) * a.N;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (col0 + j * 4 < a.N)            // N is a multiple of 8
+              __stcg(reinterpret_cast<ulonglong2*>(p + col0 + j * 4), make_ulonglong2(sum[2 * j], sum[2 * j + 1]));
+        }
+      } else if (ok && nvalid > 0) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int col = col0 + b * 64;
@@ -331,6 +358,7 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   p.n = a.n;
   p.E = a.E;
   p.C = (int)a.C;
+  p.n_max = (int)a.rows;
   p.K = a.K;
   p.N = a.N;
   p.KB = (a.K + 127) / 128;
@@ -338,11 +366,17 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   p.xs = a.xs;
   p.ws = a.ws;
   p.y = static_cast<__nv_bfloat16*>(a.y);
+  p.splits = split_count(a.E, a.rows, a.N, p.KB, kBlockUs, a.num_sms);
+  p.rows = (int)a.rows;
+  p.part = a.part;
   p.err = a.err;
   p.limit_ns = a.limit_ns;
-  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+  auto kern = p.splits > 1 ? fp8_pair_kernel<true> : fp8_pair_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fp8_pair_kernel, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
+  e = launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return split_join(a.part, a.y, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
 }
 
 }  // namespace moe

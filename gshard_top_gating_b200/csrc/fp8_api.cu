@@ -59,7 +59,9 @@ moe_status moe_fp8_create(moe_fp8_handle* out, int32_t E, int64_t C_max, int64_t
   BufferCarver c{nullptr};
   for (int pass = 0; ce == cudaSuccess && pass < 2; ++pass) {
     c.off = 0;
-    h->part = c.take<float>(few_rows_workspace(C_max, true, h->num_sms, &h->ncount));
+    const size_t few = few_rows_workspace(true, h->num_sms, &h->ncount);
+    const size_t split = split_workspace(E, (int)N, h->num_sms);
+    h->part = c.take<float>(few > split ? few : split);
     h->err = c.take<unsigned>(1 + h->ncount);     // the error word, then the counts
     h->count = h->err + 1;
     if (pass == 0) {

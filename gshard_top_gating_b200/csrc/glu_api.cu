@@ -102,8 +102,9 @@ moe_status moe_glu_create(moe_glu_handle* out, int32_t E, int64_t C_max, int64_t
     c.off = 0;
     h->h = c.take<char>((size_t)E * Cp * H * act_bytes_of(act));
     if (act == MOE_BF16) {
-      const size_t parts = few_rows_workspace(C_max, false, h->num_sms, &h->ncount);
-      h->part = c.take<float>(parts);
+      const size_t few = few_rows_workspace(false, h->num_sms, &h->ncount);
+      const size_t split = split_workspace(E, (int)M, h->num_sms);
+      h->part = c.take<float>(few > split ? few : split);
     }
     h->err = c.take<unsigned>(1 + h->ncount);     // the error word, then the counts
     h->count = h->err + 1;

@@ -72,6 +72,8 @@ struct PairArgs {
   int tailA, tailB;      // kDw: the last, partial 64-row block comes from the tail maps
   int store_zero;        // kDw: experts without rows get zeros (else keep what they hold)
   __nv_bfloat16* D;      // output, for the row-by-row stores (kDown, kDx)
+  int splits, rows;      // kDown, kDx: shares of the depth (split.cu); most rows an expert holds
+  float* part;           // splits > 1: [splits][E, rows, N] fp32 sums instead of D
   unsigned* err;
   uint64_t limit_ns;
 };
@@ -132,6 +134,21 @@ __device__ __forceinline__ void store_plain(const CUtensorMap* tmD, uint32_t tme
         tma_store_2d_hint(tmD, tile, col, (int)row0, l2_policy_evict_first());
         bulk_commit();
       }
+    }
+  }
+}
+
+// The fp32 sums of one warp's rows (this lane's at p, N columns from column col0).
+__device__ __forceinline__ void store_sums(uint32_t tmem, float* p, int col0, int N, bool live) {
+#pragma unroll 1
+  for (int b = 0; b < PN / 32 && col0 + b * 32 < N; ++b) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(tmem + b * 32, r);
+    tmem_ld_wait();
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        __stcg(reinterpret_cast<uint4*>(p + col0 + b * 32) + j, make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]));
     }
   }
 }
@@ -220,6 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
   constexpr bool UP = MODE == kUp || MODE == kUpSave;
   constexpr bool BKM = MODE == kDh || MODE == kDx;     // B's depth is contiguous
   constexpr int COLS = UP ? 128 : PN;                  // output columns of a tile
+  constexpr bool SPLIT = MODE == kDown || MODE == kDx; // a tile's depth may be cut into shares
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
@@ -245,6 +263,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int NT = (a.N + COLS - 1) / COLS;
   const int KB = a.K / BK;
+  const int splits = SPLIT ? a.splits : 1;
+  // item -> tile, and the item's blocks of depth
+  auto tile_of = [&](int item) { return SPLIT && splits > 1 ? item / splits : item; };
+  auto depth_of = [&](int item, int& from, int& to) {
+    const int s = SPLIT && splits > 1 ? item % splits : 0;
+    from = s == 0 ? 0 : KB * s / splits;
+    to = s + 1 == splits ? KB : KB * (s + 1) / splits;
+    return s;
+  };
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -305,12 +332,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
       uint32_t ph = 0;
       bool ok = true;
       int e, mt, nt;
-      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs) {
+      for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs) {
         const int rowA = (int)(e * a.Ca) + mt * PM + (int)rank * 128;
         // first column of this CTA's half of B: the same 128 elements of Wg or of Wu, or 128
         // of the tile's 256 columns
         const int colB = UP ? (int)rank * a.N + nt * COLS : nt * COLS + (int)rank * 128;
-        for (int kb = 0; kb < KB; ++kb) {
+        int from, to;
+        depth_of(tile, from, to);
+        for (int kb = from; kb < to; ++kb) {
           if (*abort_flag || !mbar_wait(empty_bar(s), ph ^ 1u, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
@@ -344,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
       uint32_t ph = 0;
       bool ok = true;
       int e, mt, nt, i = 0;
-      for (int tile = pair; ok && it.decode(tile, e, mt, nt); tile += npairs, ++i) {
+      for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs, ++i) {
         const int acc = i & 1;
         const uint32_t aph = (i >> 1) & 1;
         if (*abort_flag || !mbar_wait(tempty_bar(acc), aph ^ 1u, a.err, a.limit_ns)) {
@@ -354,7 +383,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * PN;
-        for (int kb = 0; kb < KB; ++kb) {
+        int from, to;
+        depth_of(tile, from, to);
+        for (int kb = from; kb < to; ++kb) {
           if (*abort_flag || !mbar_wait(full_bar(s), ph, a.err, a.limit_ns)) {
             *abort_flag = 1;
             ok = false;
@@ -368,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
             const uint64_t ad = desc_sw128(sa + kk * 32u, 16u, 1024u);
             const uint64_t bd = BKM ? desc_sw128(sb + kk * 32u, 16u, 1024u)
                                     : desc_sw128(sb + kk * 2048u, 8192u, 1024u);
-            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kb | kk) != 0);
+            tc_mma_f16_pair(d_tmem, ad, bd, idesc, kb != from || kk != 0);
           }
           tc_commit_pair(empty_bar(s), 0x3);
           if (++s == STAGES) {
@@ -392,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, i = 0;
     uint32_t gph = 0;            // kDh: phase bits of the two (g, u) buffers
-    for (int tile = pair; it.decode(tile, e, mt, nt); tile += npairs, ++i) {
+    for (int tile = pair; it.decode(tile_of(tile), e, mt, nt); tile += npairs, ++i) {
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1;
       const int local = mt * PM + (int)rank * 128 + q * 32;     // row within the expert
@@ -478,7 +509,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
         }
         if (!ok) *abort_flag = 1;
       } else {
-        if (nvalid > 0) store_plain(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
+        if (SPLIT && splits > 1) {
+          int from, to;
+          const int s = depth_of(tile, from, to);
+          if (nvalid > 0)
+            store_sums(tm, a.part + (((int64_t)s * a.E + e) * a.rows + local + lane) * a.N, col0, a.N, lane < nvalid);
+        } else if (nvalid > 0) store_plain(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -731,10 +767,23 @@ PairArgs pair_args(const GluArgs& a) {
   PairArgs p{};
   p.n = a.n;
   p.E = a.E;
-  p.C = (int)a.C;
+  p.C = (int)a.rows;      // no expert holds more
   p.err = a.err;
   p.limit_ns = a.limit_ns;
   return p;
+}
+
+// kDown, kDx: with too few tiles for the device, in shares of the depth.
+constexpr double kBlockUs = 0.28;      // 256 x 256 x 64 on a pair
+template <int MODE>
+cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, PairArgs p,
+                         const GluArgs& a, void* out) {
+  p.splits = split_count(a.E, a.rows, p.N, p.K / BK, kBlockUs, a.num_sms);
+  p.rows = (int)a.rows;
+  p.part = a.part;
+  const cudaError_t e = launch_pair<MODE, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return split_join(a.part, out, a.n, a.E, a.rows, a.C, p.N, p.splits, a.st);
 }
 
 uint64_t rows(int E, int64_t per) { return (uint64_t)E * (uint64_t)per; }
@@ -789,7 +838,7 @@ cudaError_t glu_down_bf16(const GluArgs& a) {
   p.K = a.H;
   p.N = a.M;
   p.D = static_cast<__nv_bfloat16*>(a.y);
-  return launch_pair<kDown, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
+  return launch_split<kDown>(tmA, tmB, tmD, p, a, a.y);
 }
 
 cudaError_t glu_tail_bf16(const GluArgs& a) {
@@ -826,7 +875,7 @@ cudaError_t glu_dx_bf16(const GluArgs& a) {
   p.K = 2 * a.H;
   p.N = a.M;
   p.D = static_cast<__nv_bfloat16*>(a.dx);
-  return launch_pair<kDx, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
+  return launch_split<kDx>(tmA, tmB, tmD, p, a, a.dx);
 }
 
 cudaError_t glu_dw2_bf16(const GluArgs& a) {

@@ -285,8 +285,8 @@ struct GluArgs {
   void* tx;              // bf16: [E, 64, M] copies of the last partial 64-row block of x and of
   void* tdy;             //   dy, or null where those rows hold zeros up to a multiple of 64
   bool skip_empty;       // experts without rows leave dW13[e], dW2[e] as they are (else zeros)
-  float* part;           // few_rows.cu: partial sums and arrival counts (few_rows_workspace)
-  unsigned* count;
+  float* part;           // partial sums (few_rows_workspace, split_workspace: the larger)
+  unsigned* count;       // few_rows.cu: arrival counts
   unsigned* err;
   uint64_t limit_ns;
   int num_sms;
@@ -318,8 +318,8 @@ struct Fp8Args {
   const void* wq;        // [E, N, K] e4m3
   const float* ws;       // [E, ceil(N/128), ceil(K/128)]
   void* y;               // [E, C, N] bf16
-  float* part;           // few_rows.cu: partial sums and arrival counts (few_rows_workspace)
-  unsigned* count;
+  float* part;           // partial sums (few_rows_workspace, split_workspace: the larger)
+  unsigned* count;       // few_rows.cu: arrival counts
   unsigned* err;
   uint64_t limit_ns;
   int num_sms;
@@ -327,10 +327,17 @@ struct Fp8Args {
 };
 cudaError_t fp8_matmul(const Fp8Args& a);       // few_rows.cu or 256 x 256 tiles
 cudaError_t fp8_pair(const Fp8Args& a);         // 256 x 256 tiles
+// split.cu: into how many shares of the depth (KB blocks of block_us each on a tile) the 256 x 256
+// tiles of a product are cut (1: not at all), the floats of workspace its sums need at most,
+// and the kernel that adds them: part [splits][E, rows, N] -> y [E, C, N].
+int split_count(int E, int64_t rows, int N, int KB, double block_us, int num_sms);
+size_t split_workspace(int E, int N, int num_sms);
+cudaError_t split_join(const float* part, void* y, const int32_t* n, int E, int64_t rows, int64_t C, int N, int splits,
+                       cudaStream_t st);
 // few_rows.cu: the same products (gated experts' up and down in bf16, the 8-bit one) for few
 // rows.  Workspace: floats of partial sums (returned) and counts, zero before the first
 // launch; every launch leaves the counts zero.
-size_t few_rows_workspace(int64_t C_max, bool fp8, int num_sms, size_t* counts);
+size_t few_rows_workspace(bool fp8, int num_sms, size_t* counts);
 cudaError_t glu_few_up(const GluArgs& a);
 cudaError_t glu_few_down(const GluArgs& a);
 cudaError_t fp8_few(const Fp8Args& a);

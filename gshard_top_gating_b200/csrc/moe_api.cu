@@ -171,8 +171,13 @@ size_t carve(moe_layer* h, char* base) {
   R.psum = c.take<float>(nchunk * E);
   R.lse2 = c.take<float>(nchunk);
   R.losses = c.take<float>(2);
-  const size_t parts =
-      h->gated && h->act == MOE_BF16 ? few_rows_workspace(h->Cbuf, h->fp8, h->num_sms, &h->nfcount) : 0;
+  size_t parts = 0;
+  if (h->gated && h->act == MOE_BF16) {
+    parts = few_rows_workspace(h->fp8, h->num_sms, &h->nfcount);
+    const size_t s1 = split_workspace(h->E, (int)h->M, h->num_sms);
+    const size_t s2 = h->fp8 ? split_workspace(h->E, 2 * (int)h->H, h->num_sms) : 0;
+    for (size_t s : {s1, s2}) parts = s > parts ? s : parts;
+  }
   R.err = c.take<unsigned>(1 + h->nfcount);     // the error word, then the arrival counts
   h->fcount = R.err ? R.err + 1 : nullptr;
   R.dest = c.take<int32_t>(S * k);

@@ -134,6 +134,9 @@ CASES = [
     (16, 64, 2048, 384, [64, 33, 0, 1] * 4),
     (1, 1, 4096, 1024, [1]),
     (2, 30, 1168, 264, [30, 19]),
+    (1, 333, 4112, 520, [333]),                              # few tiles: the depth is cut into shares
+    (2, 130, 3088, 1000, [129, 7]),
+    (1, 100, 4096, 512, [100]),
     (32, 9, 2048, 1544, [i % 10 for i in range(32)]),        # long shares: part of the work is fetched
 ]
 

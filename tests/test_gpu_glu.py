@@ -130,6 +130,8 @@ CASES = [
     (32, 1, 512, 1024, [int(i in (9, 13)) for i in range(32)]),
     (3, 100, 576, 704, [100, 64, 1]),
     (2, 128, 192, 1216, [128, 33]),
+    (1, 333, 320, 2048, [333]),                                  # few tiles: the depth is cut into shares
+    (2, 100, 192, 1216, [100, 33]),
     (32, 18, 512, 1024, [(7 * i) % 19 for i in range(32)]),      # long shares: part of the work is fetched
 ]
 
