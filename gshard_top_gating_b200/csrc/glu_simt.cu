@@ -5,10 +5,11 @@
 //
 // with the rows i (or, for the weight gradients, the depth k) limited to the n rows expert e
 // holds; rows past them are neither read nor written.  A tile of T x T results per block
-// of 256 threads, T/16 x T/16 each, depth in steps of TK through shared memory with the
-// next step's operands in registers meanwhile.  A thread's columns lie in two groups, one in
-// each half of the tile: in `up` the first half holds columns of Wg and the second the same
-// columns of Wu, so that g and u of an element meet in one thread.
+// of 256 threads; the depth comes in steps of TK through shared memory, four steps in flight
+// (cp.async), each operand laid out as it lies in memory: along the depth, a thread reads four
+// k of a row at once.  A thread's columns are SIDE apart, so that neighbours read and write
+// neighbouring columns; in `up` the tile's first half holds columns of Wg and the second the
+// same columns of Wu, so that g and u of an element meet in one thread.
 #include "glu.cuh"
 #include "internal.h"
 
@@ -33,16 +34,31 @@ struct SimtArgs {
   int skip_empty;          // weight gradients of an expert without rows stay as they are
 };
 
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+constexpr int kSteps = 4;      // steps of the depth in flight
+
+// Floats of one operand's step: rows of TK (its depth contiguous) or of T values, padded by 16
+// bytes, which keeps both the copies' alignment and the reads free of bank conflicts.
+template <int T, int TK>
+constexpr int step_floats(bool along_k) { return along_k ? T * (TK + 4) : TK * (T + 4); }
+template <int T, int TK, bool AT, bool BT>
+constexpr size_t simt_smem() { return kSteps * (step_floats<T, TK>(!AT) + step_floats<T, TK>(BT)) * sizeof(float); }
+
 // AT: A's rows are contiguous (A(i, k) at k * lda + i), else its depth (i * lda + k).
 // BT: B's depth is contiguous (B(k, j) at j * ldb + k), else its columns (k * ldb + j).
 template <int T, int TK, bool AT, bool BT, int EPI, int FN>
-__global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
-  // small tiles: four groups of 64 threads take a quarter of each step's depth each, so that
-  // every thread still has 4 x 4 results (with 2 x 2, shared-memory loads bound the step)
-  constexpr int KS = T == 32 ? 4 : 1, SIDE = T == 32 ? 8 : 16;
-  constexpr int R = T / SIDE, G = T / (2 * SIDE);       // rows and columns-per-half of a thread
+__global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g) {
   pdl_wait();
   pdl_trigger();
+  // smaller tiles: four groups of 64 threads take a quarter of each step's depth each, so that
+  // a thread still has 8 x 8 (4 x 4) results; with a quarter of them, shared-memory loads
+  // bound the step
+  constexpr int KS = T == 128 ? 1 : 4, SIDE = T == 128 ? 16 : 8;
+  constexpr int R = T / SIDE, W = T / SIDE;   // rows and columns of a thread
+  constexpr int FA = step_floats<T, TK>(!AT), FB = step_floats<T, TK>(BT);
   const int e = blockIdx.z;
   const int n = min(max(g.n[e], 0), g.C);
   const int rows = g.rows ? g.rows : n, K = g.K ? g.K : n;
@@ -52,129 +68,142 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
   if (i0 >= rows || (g.skip_empty && n == 0)) return;
   const float* A = g.A + e * g.a_z;
   const float* B = g.B + e * g.b_z;
-  __shared__ __align__(16) float shared[2][TK][T + 4];
-  auto& As = shared[0];
-  auto& Bs = shared[1];
+  extern __shared__ __align__(16) float simt_shared[];
+  float* const As = simt_shared;
+  float* const Bs = simt_shared + kSteps * FA;
   const int tid = threadIdx.x, ks = tid / (SIDE * SIDE);
   const int tx = tid % SIDE, ty = tid / SIDE % SIDE;
-  constexpr int L = T * TK / (4 * kThreads);   // float4 loads per thread and operand
-  float4 ra[L], rb[L];
 
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      const int idx = tid + l * kThreads;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto load = [&](int step) {
+    const int k0 = step * TK;
+    float* as = As + step % kSteps * FA;
+    float* bs = Bs + step % kSteps * FB;
+    for (int idx = tid; idx < T * TK / 4; idx += kThreads) {
       if (AT) {            // four rows i of one k
-        const int k = k0 + idx / (T / 4), i = i0 + idx % (T / 4) * 4;
-        if (k < K && i < rows) v = *reinterpret_cast<const float4*>(A + (int64_t)k * g.lda + i);
+        const int k = idx / (T / 4), i = idx % (T / 4) * 4;
+        const bool in = k0 + k < K && i0 + i < rows;
+        cp_async16(as + k * (T + 4) + i, in ? A + (int64_t)(k0 + k) * g.lda + i0 + i : A, in);
       } else {             // four k of one row i
-        const int i = i0 + idx / (TK / 4), k = k0 + idx % (TK / 4) * 4;
-        if (i < rows && k < K) v = *reinterpret_cast<const float4*>(A + (int64_t)i * g.lda + k);
-      }
-      ra[l] = v;
-      v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (BT) {
-        const int j = j0 + idx / (TK / 4), k = k0 + idx % (TK / 4) * 4;
-        if (j < g.cols && k < K) v = *reinterpret_cast<const float4*>(B + (int64_t)j * g.ldb + k);
-      } else {
-        const int k = k0 + idx / (T / 4);
-        int j = idx % (T / 4) * 4;
-        bool in;
-        if (EPI == kSUp) {
-          in = j0 + (j & (CW - 1)) < g.H;
-          j = (j < CW ? j0 : g.H + j0 - CW) + j;
-        } else {
-          j += j0;
-          in = j < g.cols;
-        }
-        if (k < K && in) v = *reinterpret_cast<const float4*>(B + (int64_t)k * g.ldb + j);
-      }
-      rb[l] = v;
-    }
-  };
-  auto put = [&](float (&S)[TK][T + 4], const float4 (&r)[L], bool along_k) {
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      const int idx = tid + l * kThreads;
-      if (along_k) {
         const int i = idx / (TK / 4), k = idx % (TK / 4) * 4;
-        S[k][i] = r[l].x;
-        S[k + 1][i] = r[l].y;
-        S[k + 2][i] = r[l].z;
-        S[k + 3][i] = r[l].w;
+        const bool in = i0 + i < rows && k0 + k < K;
+        cp_async16(as + i * (TK + 4) + k, in ? A + (int64_t)(i0 + i) * g.lda + k0 + k : A, in);
+      }
+      if (BT) {
+        const int j = idx / (TK / 4), k = idx % (TK / 4) * 4;
+        const bool in = j0 + j < g.cols && k0 + k < K;
+        cp_async16(bs + j * (TK + 4) + k, in ? B + (int64_t)(j0 + j) * g.ldb + k0 + k : B, in);
       } else {
-        *reinterpret_cast<float4*>(&S[idx / (T / 4)][idx % (T / 4) * 4]) = r[l];
+        const int k = idx / (T / 4), j = idx % (T / 4) * 4;
+        const int col = EPI == kSUp ? (j < CW ? j0 + j : g.H + j0 + j - CW) : j0 + j;
+        const bool in = k0 + k < K && (EPI == kSUp ? j0 + (j < CW ? j : j - CW) < g.H : j0 + j < g.cols);
+        cp_async16(bs + k * (T + 4) + j, in ? B + (int64_t)(k0 + k) * g.ldb + col : B, in);
       }
     }
   };
 
-  float acc[R][2 * G] = {};
-  load(0);
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    put(As, ra, !AT);
-    put(Bs, rb, BT);
-    __syncthreads();
-    if (k0 + TK < K) load(k0 + TK);
+  const int steps = (K + TK - 1) / TK;
 #pragma unroll
-    for (int kk = 0; kk < TK / KS; ++kk) {
-      const int k = ks * (TK / KS) + kk;
-      float av[R], bv[2 * G];
+  for (int s = 0; s < kSteps - 1; ++s) {
+    if (s < steps) load(s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  float acc[R][W] = {};
+  for (int step = 0; step < steps; ++step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 2) : "memory");
+    __syncthreads();                 // this step is here for all, and all have read the one that `load` overwrites
+    if (step + kSteps - 1 < steps) load(step + kSteps - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const float* as = As + step % kSteps * FA;
+    const float* bs = Bs + step % kSteps * FB;
 #pragma unroll
-      for (int r = 0; r < R; ++r) av[r] = As[k][ty * R + r];
+    for (int kq = 0; kq < TK / KS; kq += 4) {
+      const int k = ks * (TK / KS) + kq;
+      float av[4][R], bv[4][W];
+      if (AT) {
 #pragma unroll
-      for (int c = 0; c < G; ++c) {
-        bv[c] = Bs[k][tx * G + c];
-        bv[G + c] = Bs[k][T / 2 + tx * G + c];
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int r = 0; r < R; r += 4)
+            *reinterpret_cast<float4*>(&av[d][r]) = *reinterpret_cast<const float4*>(as + (k + d) * (T + 4) + ty * R + r);
+      } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(as + (ty * R + r) * (TK + 4) + k);
+          av[0][r] = v.x;
+          av[1][r] = v.y;
+          av[2][r] = v.z;
+          av[3][r] = v.w;
+        }
+      }
+      if (BT) {
+#pragma unroll
+        for (int c = 0; c < W; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(bs + (tx + SIDE * c) * (TK + 4) + k);
+          bv[0][c] = v.x;
+          bv[1][c] = v.y;
+          bv[2][c] = v.z;
+          bv[3][c] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int c = 0; c < W; ++c) bv[d][c] = bs[(k + d) * (T + 4) + tx + SIDE * c];
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int c = 0; c < 2 * G; ++c) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int c = 0; c < W; ++c) acc[r][c] = fmaf(av[d][r], bv[d][c], acc[r][c]);
     }
-    __syncthreads();
   }
 
   if constexpr (KS > 1) {
-    // the groups' sums meet in the operands' memory; group ks keeps row ks of each 4 x 4
-    static_assert(KS == R && KS * T * T <= 2 * TK * (T + 4), "the sums fit into the operands' memory");
-    float* sums = &shared[0][0][0];            // [group][thread][R][2 G]; the last step's reads are done
+    // the groups' sums meet in the operands' memory; group ks keeps rows ks, ks + 4, ...
+    static_assert(KS * T * T <= kSteps * (FA + FB), "the sums fit into the operands' memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* sums = simt_shared;
     const int t0 = tid % (SIDE * SIDE);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < 2 * G; ++c) sums[((r * 2 * G + c) * KS + ks) * SIDE * SIDE + t0] = acc[r][c];
+      for (int c = 0; c < W; ++c) sums[((r * W + c) * KS + ks) * SIDE * SIDE + t0] = acc[r][c];
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 2 * G; ++c) {
-      float s = 0.f;
+    for (int r = 0; r < R; ++r)
+      if (r % KS == ks) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) s += sums[((ks * 2 * G + c) * KS + k) * SIDE * SIDE + t0];
+        for (int c = 0; c < W; ++c) {
+          float s = 0.f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) acc[r][c] = s;      // one of the rows below is used: r = ks
-    }
+          for (int k = 0; k < KS; ++k) s += sums[((r * W + c) * KS + k) * SIDE * SIDE + t0];
+          acc[r][c] = s;
+        }
+      }
   }
   float* D = g.D + e * g.d_z;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = i0 + ty * R + r;
-    if (i >= rows || (KS > 1 && r != ks)) continue;
+    if (i >= rows || (KS > 1 && r % KS != ks)) continue;
     if (EPI == kSUp) {
 #pragma unroll
-      for (int c = 0; c < G; ++c) {
-        const int j = j0 + tx * G + c;
+      for (int c = 0; c < W / 2; ++c) {
+        const int j = j0 + tx + SIDE * c;
         if (j >= g.H) continue;
-        D[(int64_t)i * g.ldd + j] = glu_f<FN, false>(acc[r][c]) * acc[r][G + c];
+        D[(int64_t)i * g.ldd + j] = glu_f<FN, false>(acc[r][c]) * acc[r][W / 2 + c];
         if (g.gu) {
           float* gu = g.gu + e * g.gu_z + (int64_t)i * 2 * g.H;
           gu[j] = acc[r][c];
-          gu[g.H + j] = acc[r][G + c];
+          gu[g.H + j] = acc[r][W / 2 + c];
         }
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 2 * G; ++c) {
-        const int j = j0 + (c < G ? tx * G + c : T / 2 + tx * G + c - G);
+      for (int c = 0; c < W; ++c) {
+        const int j = j0 + tx + SIDE * c;
         if (j >= g.cols) continue;
         if (EPI == kSDh) {
           const float* gu = g.gu + e * g.gu_z + (int64_t)i * 2 * g.H;
@@ -190,19 +219,30 @@ __global__ void __launch_bounds__(kThreads) glu_simt_kernel(const SimtArgs g) {
   }
 }
 
+template <int T, int TK, bool AT, bool BT, int EPI, int FN>
+cudaError_t launch_tile(const SimtArgs& g, dim3 grid, cudaStream_t st) {
+  auto kern = glu_simt_kernel<T, TK, AT, BT, EPI, FN>;
+  constexpr size_t smem = simt_smem<T, TK, AT, BT>();
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, grid, dim3(kThreads), smem, st, g);
+}
+
 // Tiles of 128 x 128 when they fill the device twice over, else of 64 x 64 when those fill it,
-// else of 32 x 32 with four times the depth per step: small products are bound by the
+// else of 32 x 32: small products are bound by the
 // latency of their steps (a training step of 8 experts x 80 rows, M = 64, H = 256: 72 us with
-// 64 x 64 tiles of depth 16 throughout, 55 us).
+// 64 x 64 tiles and one step in flight, 39 us).
 template <bool AT, bool BT, int EPI, int FN>
 cudaError_t launch(const SimtArgs& g, int64_t rows, int cols, int E, int num_sms, cudaStream_t st) {
   auto tiles = [&](int T) { return (rows + T - 1) / T * ((cols + T - 1) / T) * E; };
   const int T = tiles(128) >= 2 * num_sms ? 128 : tiles(64) >= num_sms ? 64 : 32;
   const int cw = EPI == kSUp ? T / 2 : T;
   const dim3 grid((cols / (EPI == kSUp ? 2 : 1) + cw - 1) / cw, (unsigned)((rows + T - 1) / T), E);
-  if (T == 128) return launch_pdl(glu_simt_kernel<128, 16, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
-  if (T == 64) return launch_pdl(glu_simt_kernel<64, 16, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
-  return launch_pdl(glu_simt_kernel<32, 64, AT, BT, EPI, FN>, grid, dim3(kThreads), 0, st, g);
+  if (T == 128) return launch_tile<128, 16, AT, BT, EPI, FN>(g, grid, st);
+  if (T == 64) return launch_tile<64, 32, AT, BT, EPI, FN>(g, grid, st);
+  return launch_tile<32, 32, AT, BT, EPI, FN>(g, grid, st);
 }
 
 template <bool AT, bool BT, int EPI>
