@@ -129,11 +129,9 @@ def _check(fn: str, status: int) -> None:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        return t.data_ptr()
+    return t
 
 
 def _stream(stream) -> int | None:
@@ -428,7 +426,9 @@ def moe_glu_destroy(h) -> None:
 
 
 def moe_glu_forward(h, C, x, nrows, y, stream=None) -> None:
-    _check("moe_glu_forward", lib.moe_glu_forward(h, C, _ptr(x), _ptr(nrows), _ptr(y), _stream(stream)))
+    s = lib.moe_glu_forward(h, C, _ptr(x), _ptr(nrows), _ptr(y), _stream(stream))
+    if s:
+        _check("moe_glu_forward", s)
 
 
 def moe_glu_enable_backward(h) -> None:
@@ -471,7 +471,9 @@ def moe_fp8_destroy(h) -> None:
 
 
 def moe_fp8_matmul(h, C, xq, xs, nrows, y, stream=None) -> None:
-    _check("moe_fp8_matmul", lib.moe_fp8_matmul(h, C, _ptr(xq), _ptr(xs), _ptr(nrows), _ptr(y), _stream(stream)))
+    s = lib.moe_fp8_matmul(h, C, _ptr(xq), _ptr(xs), _ptr(nrows), _ptr(y), _stream(stream))
+    if s:
+        _check("moe_fp8_matmul", s)
 
 
 def moe_fp8_check(h, stream=None) -> None:

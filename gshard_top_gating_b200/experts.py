@@ -19,17 +19,20 @@ ACTIVATIONS = {"silu": L.MOE_GLU_SILU, "gelu": L.MOE_GLU_GELU, "relu": L.MOE_GLU
 
 
 def check_tensor(name, t, shape, dtype, device) -> None:
-    if t.device != device or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}, "
                          f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def launch_on(device, stream, tensors, call):
     """call(raw stream) with the operator's device current and `stream` (default: that device's
     current stream) the one that new tensors are allocated on; tensors of other streams that
     the call uses are recorded on it."""
-    if stream is None and torch.cuda.current_device() == device.index:     # the usual call, without contexts
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is None and _current_device() == device.index:     # the usual call, without contexts
+        return call(_current_stream(device.index))
     with torch.cuda.device(device):
         current = torch.cuda.current_stream(device)
         if stream is None:
@@ -64,8 +67,10 @@ class GatedExperts:
     def _rows(self, name, t, C=None):
         if t.dim() != 3:
             raise ValueError(f"{name} must be [E, C, M]")
-        check_tensor(name, t, (self.E, t.shape[1] if C is None else C, self.M), self.act, self.device)
-        return t.shape[1]
+        if C is None:
+            C = t.shape[1]
+        check_tensor(name, t, (self.E, C, self.M), self.act, self.device)
+        return C
 
     def __call__(self, x: torch.Tensor, counts: torch.Tensor, out: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:

@@ -17,6 +17,7 @@ from .experts import check_tensor, launch_on
 
 BLOCK = 128
 E4M3 = torch.float8_e4m3fn
+_SOURCES = (torch.bfloat16, torch.float32)
 
 
 def blocks(n: int) -> int:
@@ -24,7 +25,7 @@ def blocks(n: int) -> int:
 
 
 def _source(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    if t.dtype not in _SOURCES:
         raise TypeError(f"{name} must be float32 or bfloat16")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -34,20 +35,21 @@ def quantize_rows(x: torch.Tensor, out=None, stream=None):
     """(q, s) of the rows of x [..., K]: q e4m3 like x, s float32 [..., ceil(K/128)]; new
     tensors, or the pair `out`."""
     _source(x, "x")
-    if x.dim() < 1:
+    shape, device = x.shape, x.device
+    if not shape:
         raise ValueError("x must have rows")
-    K = x.shape[-1]
-    sshape = tuple(x.shape[:-1]) + (blocks(K),)
+    K = shape[-1]
+    sshape = (shape[0], (K + 127) // 128) if len(shape) == 2 else (*shape[:-1], blocks(K))
     if out is not None:
-        check_tensor("q", out[0], x.shape, E4M3, x.device)
-        check_tensor("s", out[1], sshape, torch.float32, x.device)
+        check_tensor("q", out[0], shape, E4M3, device)
+        check_tensor("s", out[1], sshape, torch.float32, device)
 
     def call(st):
-        q, s = out if out is not None else (torch.empty(x.shape, dtype=E4M3, device=x.device),
-                                            torch.empty(sshape, dtype=torch.float32, device=x.device))
+        q, s = out if out is not None else (torch.empty(shape, dtype=E4M3, device=device),
+                                            torch.empty(sshape, dtype=torch.float32, device=device))
         L.moe_fp8_quantize_rows(x.numel() // K if K else 0, K, x, q, s, st)
         return q, s
-    return launch_on(x.device, stream, (x, *(out or ())), call)
+    return launch_on(device, stream, (x, *(out or ())), call)
 
 
 def quantize_weights(W: torch.Tensor, stream=None):
@@ -85,7 +87,7 @@ class Fp8Matmul:
         `out` stay as they are; of a new tensor they are unset."""
         if xq.dim() != 3:
             raise ValueError("xq must be [E, C, K]")
-        C = xq.shape[1]
+        C = xq.size(1)
         check_tensor("xq", xq, (self.E, C, self.K), E4M3, self.device)
         check_tensor("xs", xs, (self.E, C, blocks(self.K)), torch.float32, self.device)
         check_tensor("counts", counts, (self.E,), torch.int32, self.device)
