@@ -273,3 +273,41 @@ def test_refusals():
         quantize_rows(torch.zeros(32, 3, device="cuda").t())
     q, s = quantize_rows(torch.zeros(0, 32, device="cuda"))
     assert q.shape == (0, 32) and s.shape == (0, 1)
+
+
+def test_offsets_past_32_bits():
+    """Rows of more than 2^31 values through the quantiser and the product."""
+    from gshard_top_gating_b200.fp8 import quantize_rows, quantize_weights
+    R, K, N = 300_100, 7168, 64
+    free, _ = torch.cuda.mem_get_info()
+    if free < 20 << 30:
+        pytest.skip("needs 20 GB")
+    assert R * K > 2**31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(R, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q, s = quantize_rows(x)
+    rows = [0, 1, R // 2, R - 2, R - 1]
+    qr, a = cpu_quantize(x[rows].cpu())
+    assert torch.equal(bits(q[rows]), bits(qr))
+    W = torch.empty(1, K, N, dtype=torch.bfloat16, device="cuda").normal_(0, K**-0.5, generator=g)
+    wq, ws = quantize_weights(W)
+    n = torch.tensor([R - 1], dtype=torch.int32, device="cuda")
+    y = product(R, wq, ws)(q[None], s[None], n, out=torch.full((1, R, N), 7.0, dtype=torch.bfloat16, device="cuda"))
+    for r in rows[:-1]:
+        want = values(q[r:r + 1], s[r:r + 1], 1) @ values(wq[0], ws[0], 128).T
+        assert float((y[0, r].double() - want[0]).norm() / want.norm()) <= 1.05 * U
+    assert bool((y[0, R - 1] == 7.0).all())
+
+
+def test_misaligned_pointers_are_refused():
+    from gshard_top_gating_b200 import _lib as L
+    from gshard_top_gating_b200.fp8 import quantize_rows
+    buf = torch.zeros(64 * 4 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(L.MoeError) as err:
+        quantize_rows(buf[1:257].view(4, 64))
+    assert err.value.status == L.MOE_ERR_INVALID_ARG
+    xq, xs, wq, ws, n = make(1, 4, 64, 64, [4])
+    raw = torch.zeros(4 * 64 + 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(L.MoeError) as err:
+        product(4, wq, ws)(raw[1:257].view(torch.float8_e4m3fn).view(1, 4, 64), xs, n)
+    assert err.value.status == L.MOE_ERR_INVALID_ARG

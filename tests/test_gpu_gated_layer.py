@@ -301,3 +301,34 @@ def test_refusals_in_8_bits():
     for args, act in (((q1, W2), "silu"), ((q1, q2), None), ((q2, q1), "silu"), (((q1[0], q1[1][:, :, :0]), q2), "silu")):
         with pytest.raises((TypeError, ValueError)):
             MoeLayer(64, 64, 128, 4, 2, 1.25, Wg, b, *args, activation=act)
+
+
+def test_forward_from_host_memory_and_stage_times():
+    w, x, Wg, b, W13, W2, layer = build(300, 128, 256, 4, 2, 1.25, "bf16", "silu")
+    want = layer(x)
+    xh, yh = x.cpu().pin_memory(), torch.empty(x.shape, dtype=x.dtype).pin_memory()
+    for _ in range(3):
+        layer.forward_host(xh, yh)
+    torch.cuda.synchronize()
+    assert torch.equal(yh, want.cpu())
+    L.moe_set_profiling(layer.h, True)
+    layer.enable_backward()
+    layer(x)
+    layer.backward(x, upstream_grad(w, device="cuda"))
+    assert all(t >= 0 for t in L.moe_get_stage_times(layer.h) + L.moe_get_backward_stage_times(layer.h))
+
+
+def test_two_layers_on_two_streams():
+    """Layers of their own do not share workspaces: interleaved on two streams, same results."""
+    made = [build(64, 128, 256, 8, 2, 1.25, "bf16", "silu", seed=s) for s in (1, 2)]
+    xs, layers = [m[1] for m in made], [m[-1] for m in made]
+    want = [layer(x) for layer, x in zip(layers, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        got = [torch.zeros_like(x) for x in xs]
+        torch.cuda.synchronize()
+        for layer, x, y, s in zip(layers, xs, got, streams):
+            layer(x, out=y, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

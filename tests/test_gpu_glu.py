@@ -326,3 +326,78 @@ def test_refusals():
         GatedExperts(40, W13, W2[:, :64].contiguous())
     with pytest.raises(TypeError):
         GatedExperts(40, W13.half(), W2.half())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [5, 300])
+def test_nan_and_infinity_in_a_row_stay_in_that_row(C, dtype):
+    x, dy, W13, W2, n = make(2, C, 128, 192, dtype, [C, C - 1])
+    ex = experts(C, W13, W2, "silu")
+    clean, g_clean = ex(x, n, out=torch.zeros_like(x)), ex.backward(x, n, dy, out={"dx": torch.zeros_like(x)})
+    x[0, 3, 7], x[1, 2, 0], dy[1, 1, 5] = float("nan"), float("inf"), float("nan")
+    y, g = ex(x, n, out=torch.zeros_like(x)), ex.backward(x, n, dy, out={"dx": torch.zeros_like(x)})
+    hit_y, hit_dx = {(0, 3), (1, 2)}, {(0, 3), (1, 2), (1, 1)}
+    for e in range(2):
+        for r in range(int(n[e])):
+            assert ((e, r) in hit_y) == bool(y[e, r].isnan().any()), (e, r)
+            assert ((e, r) in hit_dx) == bool(g["dx"][e, r].isnan().any()), (e, r)
+            if (e, r) not in hit_y:
+                assert torch.equal(y[e, r], clean[e, r])
+            if (e, r) not in hit_dx:
+                assert torch.equal(g["dx"][e, r], g_clean["dx"][e, r])
+
+
+def test_saturated_gates():
+    """|g| from 20 to 1e4: f(g) is g or (nearly) 0, never NaN, for every f."""
+    E, C, M, H = 1, 4, 64, 64
+    W13 = torch.zeros(E, M, 2 * H, dtype=torch.bfloat16, device="cuda")
+    W13[0, :, :H] = torch.eye(M, H)
+    W13[0, :, H:] = torch.eye(M, H)
+    W2 = torch.eye(H, M, dtype=torch.bfloat16, device="cuda")[None].contiguous()
+    x = torch.tensor([20.0, 90.0, 128.0, 1e4], device="cuda").bfloat16()[None, :, None].repeat(1, 1, M).contiguous()
+    n = torch.tensor([4], dtype=torch.int32, device="cuda")
+    for fn in ("silu", "gelu", "relu"):
+        for sign in (1.0, -1.0):
+            ex = experts(C, W13, W2, fn)
+            y = ex(sign * x, n)
+            g = ex.backward(sign * x, n, torch.ones_like(x))
+            want = x.double() ** 2 if sign > 0 else torch.zeros_like(x.double())
+            assert bool(((y.double() - want).abs() <= 2.0**-7 * want + 1e-5).all()), (fn, sign)
+            assert g["dx"].isfinite().all() and g["dW13"].isfinite().all()
+
+
+def test_offsets_past_32_bits():
+    """x and y of more than 2^31 elements: rows at the far end of both experts."""
+    E, C, M, H = 2, 1_060_000, 1024, 64
+    free, _ = torch.cuda.mem_get_info()
+    if free < 20 << 30:
+        pytest.skip("needs 20 GB")
+    assert E * C * M > 2**31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(E, C, M, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    W13 = torch.empty(E, M, 2 * H, dtype=torch.bfloat16, device="cuda").normal_(0, M**-0.5, generator=g)
+    W2 = torch.empty(E, H, M, dtype=torch.bfloat16, device="cuda").normal_(0, H**-0.5, generator=g)
+    n = torch.tensor([C, C - 77], dtype=torch.int32, device="cuda")
+    y = experts(C, W13, W2, "silu", backward=False)(x, n, out=torch.full_like(x, 7.0))
+    for e, rows in ((0, [0, 1, C // 2, C - 1]), (1, [0, C // 2, C - 79, C - 78])):
+        gu = x[e, rows].double() @ W13[e].double()
+        want = (act("silu", gu[:, :H])[0] * gu[:, H:]) @ W2[e].double()
+        got = y[e, rows].double()
+        assert float((got - want).norm() / want.norm()) <= 2 * U[torch.bfloat16]
+    assert bool((y[1, C - 77:] == 7.0).all())
+
+
+def test_misaligned_pointers_are_refused():
+    from gshard_top_gating_b200 import _lib as L
+    x, dy, W13, W2, n = make(1, 8, 64, 64, torch.bfloat16, [8])
+    ex = experts(8, W13, W2, "silu")
+    buf = torch.zeros(x.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    off = buf[1:1 + x.numel()].view(1, 8, 64)
+    for args, kw in (((off, n), {}), ((x, n), {"out": off})):
+        with pytest.raises(L.MoeError) as err:
+            ex(*args, **kw)
+        assert err.value.status == L.MOE_ERR_INVALID_ARG
+    ex(x, n)
+    with pytest.raises(L.MoeError) as err:
+        ex.backward(x, n, off)
+    assert err.value.status == L.MOE_ERR_INVALID_ARG
