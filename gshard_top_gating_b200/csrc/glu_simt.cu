@@ -74,6 +74,10 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
   const int tid = threadIdx.x, ks = tid / (SIDE * SIDE);
   const int tx = tid % SIDE, ty = tid / SIDE % SIDE;
 
+  // this thread's rows: contiguous where four of them are read at once, else SIDE apart, which
+  // spreads a warp's rows over the banks
+  auto row_of = [&](int r) { return AT ? ty * R + r : ty + SIDE * r; };
+
   auto load = [&](int step) {
     const int k0 = step * TK;
     float* as = As + step % kSteps * FA;
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
       } else {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float4 v = *reinterpret_cast<const float4*>(as + (ty * R + r) * (TK + 4) + k);
+          const float4 v = *reinterpret_cast<const float4*>(as + row_of(r) * (TK + 4) + k);
           av[0][r] = v.x;
           av[1][r] = v.y;
           av[2][r] = v.z;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
   float* D = g.D + e * g.d_z;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = i0 + ty * R + r;
+    const int i = i0 + row_of(r);
     if (i >= rows || (KS > 1 && r % KS != ks)) continue;
     if (EPI == kSUp) {
 #pragma unroll
