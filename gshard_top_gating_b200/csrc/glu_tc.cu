@@ -22,9 +22,9 @@
 //
 // Roles per CTA: warp 0 loads (TMA), warp 1 issues MMAs (the pair's first CTA) and owns TMEM,
 // warps 2..5 drain the accumulator, double buffered, while the next tile's products run; in
-// `dh`, whose epilogue evaluates f and f' and moves four more tiles, warps 2..9, each 128
-// columns (with four warps it outlasted the products: 545 against 346 us for 8 x 2048 rows,
-// M = 2048, H = 8192).  Every wait is bounded.
+// `up` and `dh`, whose epilogues evaluate f (and f') and move more tiles, warps 2..9, half of
+// the columns each (with four warps `dh` outlasted its products, 545 against 346 us for
+// 8 x 2048 rows, M = 2048, H = 8192, and `up` did for small M).  Every wait is bounded.
 #include "common.cuh"
 #include "glu.cuh"
 #include "internal.h"
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int BK = 64;                 // depth of a stage
 constexpr int PM = 256, PN = 256;      // pair tile
-constexpr int epi_warps(int mode) { return mode == 3 ? 8 : 4; }     // kDh: 8
+constexpr int epi_warps(int mode) { return mode == 0 || mode == 1 || mode == 3 ? 8 : 4; }     // kUp, kUpSave, kDh: 8
 constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 constexpr uint32_t A_BYTES = 128 * BK * 2;            // 16 KB: 128 rows of A
 constexpr uint32_t B_BYTES = 128 * BK * 2;            // 16 KB: 128 columns of B
@@ -47,14 +47,17 @@ constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;        // shared::cluster address
 
 enum { kUp = 0, kUpSave = 1, kDown = 2, kDh = 3, kDx = 4, kDw = 5 };
 
-// Store tiles per epilogue warp: h; h, g and u; one; two buffers of (g, u) of 32 columns, which
-// dg and du leave through; one; one.
-constexpr int store_tiles(int mode) { return mode == kUpSave ? 3 : mode == kDh ? 2 : 1; }
+// Shared memory of an epilogue warp: tiles of 32 rows x 32 columns for h; for h, g and u; two
+// buffers of them for g and u, which dg and du leave through; else one of 32 x 64.
+constexpr uint32_t NARROW_BYTES = 2048;
+constexpr uint32_t epi_bytes(int mode) {
+  return mode == kUp ? NARROW_BYTES : mode == kUpSave ? 3 * NARROW_BYTES : mode == kDh ? 4 * NARROW_BYTES : TILE_BYTES;
+}
 constexpr int stages(int mode) { return mode == kUpSave ? 5 : mode == kDh ? 4 : 6; }
 constexpr uint32_t kBars = 512;
 constexpr size_t smem_bytes(int mode) {
   // alignment slack, stages, store tiles, barriers, misc, tile tables
-  return 1024 + (size_t)stages(mode) * STAGE_BYTES + epi_warps(mode) * store_tiles(mode) * TILE_BYTES + kBars + 16 +
+  return 1024 + (size_t)stages(mode) * STAGE_BYTES + epi_warps(mode) * epi_bytes(mode) + kBars + 16 +
          4 * (3 * kMaxExperts + 1);
 }
 // A CTA owns its SM (see the expert GEMMs of ffn_tc.cu): no other TMEM user fits beside it.
@@ -153,57 +156,7 @@ __device__ __forceinline__ void store_sums(uint32_t tmem, float* p, int col0, in
   }
 }
 
-// g and u of one warp's 32 rows x 128 elements -> h (tmD), and with SAVE g and u as well
-// (tmD2, [.., 2H]: g at column n, u at H + n); rows past nvalid become zeros with SAVE.
-template <int FN, bool SAVE>
-__device__ __forceinline__ void store_up(const CUtensorMap* tmD, const CUtensorMap* tmD2, uint32_t tmem, uint32_t tile,
-                                         int row0, int col0, int H, int nvalid, int lane) {
-  const bool live = !SAVE || lane < nvalid;
-#pragma unroll 1
-  for (int b = 0; b < 2; ++b) {
-    const int col = col0 + b * 64;
-    if (col >= H) return;
-    if (lane == 0) bulk_wait_read0();
-    __syncwarp();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t g[32], u[32], pk[16];
-      tmem_ld_32x32b_x32(tmem + b * 64 + half * 32, g);
-      tmem_ld_32x32b_x32(tmem + 128 + b * 64 + half * 32, u);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float h0 = glu_f<FN, true>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]);
-        const float h1 = glu_f<FN, true>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]);
-        pk[j] = live ? pack_bf16x2(h0, h1) : 0u;
-      }
-      put_half(tile, lane, half, pk);
-      if (SAVE) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          pk[j] = live ? pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])) : 0u;
-        put_half(tile + TILE_BYTES, lane, half, pk);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          pk[j] = live ? pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])) : 0u;
-        put_half(tile + 2 * TILE_BYTES, lane, half, pk);
-      }
-    }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d_hint(tmD, tile, col, row0, l2_policy_evict_first());
-      if (SAVE) {
-        tma_store_2d_hint(tmD2, tile + TILE_BYTES, col, row0, l2_policy_evict_first());
-        tma_store_2d_hint(tmD2, tile + 2 * TILE_BYTES, H + col, row0, l2_policy_evict_first());
-      }
-      bulk_commit();
-    }
-  }
-}
-
 // 32 packed bf16 of this lane's row in a 32-column tile with 64-byte swizzle.
-constexpr uint32_t NARROW_BYTES = 2048;
 __device__ __forceinline__ void put_narrow(uint32_t tile, int lane, const uint32_t (&pk)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -217,6 +170,53 @@ __device__ __forceinline__ void get_narrow(uint32_t tile, int lane, uint32_t (&p
     pk[4 * j + 1] = v.y;
     pk[4 * j + 2] = v.z;
     pk[4 * j + 3] = v.w;
+  }
+}
+
+// g and u of one warp's 32 rows x 64 elements (accumulator columns tmem and tmem + 128) -> h
+// (tmD), and with SAVE g and u as well (tmD2, [.., 2H]: g at column n, u at H + n); rows past
+// nvalid become zeros with SAVE.
+template <int FN, bool SAVE>
+__device__ __forceinline__ void store_up(const CUtensorMap* tmD, const CUtensorMap* tmD2, uint32_t tmem, uint32_t tile,
+                                         int row0, int col0, int H, int nvalid, int lane) {
+  const bool live = !SAVE || lane < nvalid;
+  if (col0 >= H) return;                         // H is a multiple of 64
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    const int col = col0 + half * 32;
+    uint32_t g[32], u[32], pk[16];
+    tmem_ld_32x32b_x32(tmem + half * 32, g);
+    tmem_ld_32x32b_x32(tmem + 128 + half * 32, u);
+    if (lane == 0) bulk_wait_read0();
+    __syncwarp();
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float h0 = glu_f<FN, true>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]);
+      const float h1 = glu_f<FN, true>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]);
+      pk[j] = live ? pack_bf16x2(h0, h1) : 0u;
+    }
+    put_narrow(tile, lane, pk);
+    if (SAVE) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        pk[j] = live ? pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])) : 0u;
+      put_narrow(tile + NARROW_BYTES, lane, pk);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        pk[j] = live ? pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])) : 0u;
+      put_narrow(tile + 2 * NARROW_BYTES, lane, pk);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d_hint(tmD, tile, col, row0, l2_policy_evict_first());
+      if (SAVE) {
+        tma_store_2d_hint(tmD2, tile + NARROW_BYTES, col, row0, l2_policy_evict_first());
+        tma_store_2d_hint(tmD2, tile + 2 * NARROW_BYTES, H + col, row0, l2_policy_evict_first());
+      }
+      bulk_commit();
+    }
   }
 }
 
@@ -243,14 +243,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
   const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
   unsigned char* gbase = smem_raw + (base - raw_base);
   const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
-  const uint32_t bar0 = tiles0 + epi_warps(MODE) * store_tiles(MODE) * TILE_BYTES;
+  const uint32_t bar0 = tiles0 + epi_warps(MODE) * epi_bytes(MODE);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
   auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
   auto gu_bar = [&](int w, int i) { return bar0 + 8u * (2 * STAGES + 5 + 2 * w + i); };
-  unsigned char* misc = gbase + STAGES * STAGE_BYTES + epi_warps(MODE) * store_tiles(MODE) * TILE_BYTES + kBars;
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + epi_warps(MODE) * epi_bytes(MODE) + kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   int* tile_pre = reinterpret_cast<int*>(misc + 16);   // [E + 1]
@@ -418,8 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
   } else {
     // ------------------------------------------------------------ epilogue (from warp 2, both CTAs)
     const int q = warp & 3;
-    const int part = (warp - 2) >> 2;            // kDh: which 128 of the tile's 256 columns
-    const uint32_t tile0 = tiles0 + (warp - 2) * store_tiles(MODE) * TILE_BYTES;
+    const int part = (warp - 2) >> 2;            // kUp, kDh: which half of the tile's columns
+    const uint32_t tile0 = tiles0 + (warp - 2) * epi_bytes(MODE);
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, i = 0;
     uint32_t gph = 0;            // kDh: phase bits of the two (g, u) buffers
@@ -429,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
       const int local = mt * PM + (int)rank * 128 + q * 32;     // row within the expert
       const int64_t row0 = e * a.Cd + local;
       const int nvalid = min(32, nrows[e] - local);
-      const int col0 = nt * COLS + part * 128;
+      const int col0 = nt * COLS + part * (COLS / 2);
       if (MODE == kDh && nvalid > 0 && col0 < a.N && lane == 0) {
         bulk_wait_read0();       // the previous tile's stores have read their buffers
         load_gu(&tmD2, tile0, gu_bar(warp - 2, 0), (int)row0, col0, a.N);
@@ -448,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
       const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN;
       if constexpr (UP) {
         if (MODE == kUpSave || nvalid > 0)
-          store_up<FN, MODE == kUpSave>(&tmD, &tmD2, tm, tile0, (int)row0, col0, a.N, nvalid, lane);
+          store_up<FN, MODE == kUpSave>(&tmD, &tmD2, tm + part * 64, tile0, (int)row0, col0, a.N, nvalid, lane);
       } else if constexpr (MODE == kDh) {
         bool ok = true;
         const int nb = max(0, min(4, (a.N - col0) / 32));      // N is a multiple of 64
@@ -816,8 +816,8 @@ cudaError_t glu_up_bf16(const GluArgs& a) {
   CUtensorMap tmA, tmB, tmD, tmD2;
   if (!encode_2d(&tmA, a.x, a.M, rows(a.E, a.C), BK, 128) ||
       !encode_2d(&tmB, a.W13, 2 * (uint64_t)a.H, rows(a.E, a.M), 64, BK) ||
-      !encode_2d(&tmD, a.h, a.H, rows(a.E, a.Cp), 64, 32) ||
-      !encode_2d(&tmD2, a.gu ? a.gu : a.h, a.gu ? 2 * (uint64_t)a.H : a.H, rows(a.E, a.Cp), 64, 32))
+      !encode_2d_narrow(&tmD, a.h, a.H, rows(a.E, a.Cp), 32) ||
+      !encode_2d_narrow(&tmD2, a.gu ? a.gu : a.h, a.gu ? 2 * (uint64_t)a.H : a.H, rows(a.E, a.Cp), 32))
     return cudaErrorInvalidValue;
   PairArgs p = pair_args(a);
   p.Ca = a.C;
