@@ -376,7 +376,7 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return split_join(a.part, a.y, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
+  return split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
 }
 
 }  // namespace moe

@@ -105,6 +105,8 @@ moe_status moe_glu_create(moe_glu_handle* out, int32_t E, int64_t C_max, int64_t
       const size_t few = few_rows_workspace(false, h->num_sms, &h->ncount);
       const size_t split = split_workspace(E, (int)M, h->num_sms);
       h->part = c.take<float>(few > split ? few : split);
+    } else {
+      h->part = c.take<float>(glu_f32_workspace(h->num_sms));
     }
     h->err = c.take<unsigned>(1 + h->ncount);     // the error word, then the counts
     h->count = h->err + 1;

@@ -32,6 +32,8 @@ struct SimtArgs {
   const int32_t* n;
   int C;
   int skip_empty;          // weight gradients of an expert without rows stay as they are
+  int splits;              // shares of the depth: 1, or D is [splits][E, most rows, cols] (split.cu)
+  int64_t s_z;             // splits > 1: from one share's sums to the next
 };
 
 __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool live) {
@@ -59,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
   constexpr int KS = T == 128 ? 1 : 4, SIDE = T == 128 ? 16 : 8;
   constexpr int R = T / SIDE, W = T / SIDE;   // rows and columns of a thread
   constexpr int FA = step_floats<T, TK>(!AT), FB = step_floats<T, TK>(BT);
-  const int e = blockIdx.z;
+  const int e = blockIdx.z / g.splits, share = blockIdx.z % g.splits;
   const int n = min(max(g.n[e], 0), g.C);
   const int rows = g.rows ? g.rows : n, K = g.K ? g.K : n;
   // `up`: the tile is T/2 columns of g beside the same T/2 columns of u
@@ -105,14 +107,15 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
     }
   };
 
-  const int steps = (K + TK - 1) / TK;
+  const int all = (K + TK - 1) / TK;
+  const int from = all * share / g.splits, steps = all * (share + 1) / g.splits;
 #pragma unroll
   for (int s = 0; s < kSteps - 1; ++s) {
-    if (s < steps) load(s);
+    if (from + s < steps) load(from + s);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   float acc[R][W] = {};
-  for (int step = 0; step < steps; ++step) {
+  for (int step = from; step < steps; ++step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 2) : "memory");
     __syncthreads();                 // this step is here for all, and all have read the one that `load` overwrites
     if (step + kSteps - 1 < steps) load(step + kSteps - 1);
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) glu_simt_kernel(const SimtArgs g)
         }
       }
   }
-  float* D = g.D + e * g.d_z;
+  float* D = g.D + e * g.d_z + share * g.s_z;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = i0 + row_of(r);
@@ -238,15 +241,38 @@ cudaError_t launch_tile(const SimtArgs& g, dim3 grid, cudaStream_t st) {
 // else of 32 x 32: small products are bound by the
 // latency of their steps (a training step of 8 experts x 80 rows, M = 64, H = 256: 72 us with
 // 64 x 64 tiles and one step in flight, 39 us).
+int tile_of(int64_t rows, int cols, int E, int num_sms) {
+  auto tiles = [&](int T) { return (rows + T - 1) / T * ((cols + T - 1) / T) * E; };
+  return tiles(128) >= 2 * num_sms ? 128 : tiles(64) >= num_sms ? 64 : 32;
+}
+
 template <bool AT, bool BT, int EPI, int FN>
 cudaError_t launch(const SimtArgs& g, int64_t rows, int cols, int E, int num_sms, cudaStream_t st) {
-  auto tiles = [&](int T) { return (rows + T - 1) / T * ((cols + T - 1) / T) * E; };
-  const int T = tiles(128) >= 2 * num_sms ? 128 : tiles(64) >= num_sms ? 64 : 32;
+  const int T = tile_of(rows, cols, E, num_sms);
   const int cw = EPI == kSUp ? T / 2 : T;
-  const dim3 grid((cols / (EPI == kSUp ? 2 : 1) + cw - 1) / cw, (unsigned)((rows + T - 1) / T), E);
+  const dim3 grid((cols / (EPI == kSUp ? 2 : 1) + cw - 1) / cw, (unsigned)((rows + T - 1) / T), E * g.splits);
   if (T == 128) return launch_tile<128, 16, AT, BT, EPI, FN>(g, grid, st);
   if (T == 64) return launch_tile<64, 32, AT, BT, EPI, FN>(g, grid, st);
   return launch_tile<32, 32, AT, BT, EPI, FN>(g, grid, st);
+}
+
+// down and dx where 32 x 32 tiles leave SMs idle over a long depth: in shares of at least 256,
+// joined by one more kernel (one row, M = 64, H = 2944, forward: 38 -> 15 us; 2 x 155 rows, M = 320, H = 4800: 186 -> 139 us).
+constexpr int kShareK = 256;
+template <bool BT>
+cudaError_t launch_shares(SimtArgs g, const GluArgs& a, int K, float* out) {
+  const int64_t tiles = (a.rows + 31) / 32 * ((g.cols + 31) / 32) * a.E;
+  int64_t s = tile_of(a.rows, g.cols, a.E, a.num_sms) == 32 ? 2 * a.num_sms / tiles : 1;
+  if (s > K / kShareK) s = K / kShareK;
+  if (s < 2) return launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
+  g.splits = (int)s;
+  g.D = a.part;
+  g.ldd = g.cols;
+  g.d_z = a.rows * g.cols;
+  g.s_z = a.E * g.d_z;
+  const cudaError_t e = launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
+  if (e != cudaSuccess) return e;
+  return split_join(a.part, out, false, a.n, a.E, a.rows, a.C, g.cols, (int)s, a.st);
 }
 
 template <bool AT, bool BT, int EPI>
@@ -275,35 +301,39 @@ SimtArgs simt_args(const GluArgs& a, const void* A, int64_t a_z, int lda, const 
   g.gu = static_cast<float*>(a.gu);
   g.gu_z = a.Cp * 2 * a.H;
   g.n = a.n;
-  g.C = (int)a.C;
+  g.C = (int)a.rows;
+  g.splits = 1;
   return g;
 }
 
 }  // namespace
 
+// tiles x shares stays within two tiles of 32 x 32 per SM.
+size_t glu_f32_workspace(int num_sms) { return (size_t)2 * num_sms * 32 * 32; }
+
 cudaError_t glu_up_f32(const GluArgs& a) {
   const int64_t w = (int64_t)a.M * 2 * a.H;
   const SimtArgs g = simt_args(a, a.x, a.C * a.M, a.M, a.W13, w, 2 * a.H, a.h, a.Cp * a.H, a.H, 0, 2 * a.H, a.M);
-  return launch_fn<false, false, kSUp>(a.fn, g, a.C, 2 * a.H, a.E, a.num_sms, a.st);
+  return launch_fn<false, false, kSUp>(a.fn, g, a.rows, 2 * a.H, a.E, a.num_sms, a.st);
 }
 
 cudaError_t glu_down_f32(const GluArgs& a) {
   const int64_t w = (int64_t)a.H * a.M;
   const SimtArgs g = simt_args(a, a.h, a.Cp * a.H, a.H, a.W2, w, a.M, a.y, a.C * a.M, a.M, 0, a.M, a.H);
-  return launch<false, false, kSPlain, kGluSilu>(g, a.C, a.M, a.E, a.num_sms, a.st);
+  return launch_shares<false>(g, a, a.H, static_cast<float*>(a.y));
 }
 
 cudaError_t glu_dh_f32(const GluArgs& a) {
   const int64_t w = (int64_t)a.H * a.M;
   const SimtArgs g = simt_args(a, a.dy, a.C * a.M, a.M, a.W2, w, a.M, a.dgu, a.Cp * 2 * a.H, 2 * a.H, 0, a.H, a.M);
-  return launch_fn<false, true, kSDh>(a.fn, g, a.C, a.H, a.E, a.num_sms, a.st);
+  return launch_fn<false, true, kSDh>(a.fn, g, a.rows, a.H, a.E, a.num_sms, a.st);
 }
 
 cudaError_t glu_dx_f32(const GluArgs& a) {
   const int64_t w = (int64_t)a.M * 2 * a.H;
   const SimtArgs g =
       simt_args(a, a.dgu, a.Cp * 2 * a.H, 2 * a.H, a.W13, w, 2 * a.H, a.dx, a.C * a.M, a.M, 0, a.M, 2 * a.H);
-  return launch<false, true, kSPlain, kGluSilu>(g, a.C, a.M, a.E, a.num_sms, a.st);
+  return launch_shares<true>(g, a, 2 * a.H, static_cast<float*>(a.dx));
 }
 
 cudaError_t glu_dw2_f32(const GluArgs& a) {

@@ -301,6 +301,7 @@ cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu
 cudaError_t glu_dx_bf16(const GluArgs& a);      // dx
 cudaError_t glu_dw2_bf16(const GluArgs& a);
 cudaError_t glu_dw13_bf16(const GluArgs& a);
+size_t glu_f32_workspace(int num_sms);          // floats of partial sums (GluArgs::part)
 cudaError_t glu_up_f32(const GluArgs& a);
 cudaError_t glu_down_f32(const GluArgs& a);
 cudaError_t glu_dh_f32(const GluArgs& a);
@@ -332,8 +333,8 @@ cudaError_t fp8_pair(const Fp8Args& a);         // 256 x 256 tiles
 // and the kernel that adds them: part [splits][E, rows, N] -> y [E, C, N].
 int split_count(int E, int64_t rows, int N, int KB, double block_us, int num_sms);
 size_t split_workspace(int E, int N, int num_sms);
-cudaError_t split_join(const float* part, void* y, const int32_t* n, int E, int64_t rows, int64_t C, int N, int splits,
-                       cudaStream_t st);
+cudaError_t split_join(const float* part, void* y, bool bf16, const int32_t* n, int E, int64_t rows, int64_t C, int N,
+                       int splits, cudaStream_t st);
 // few_rows.cu: the same products (gated experts' up and down in bf16, the 8-bit one) for few
 // rows.  Workspace: floats of partial sums (returned) and counts, zero before the first
 // launch; every launch leaves the counts zero.

@@ -177,6 +177,8 @@ size_t carve(moe_layer* h, char* base) {
     const size_t s1 = split_workspace(h->E, (int)h->M, h->num_sms);
     const size_t s2 = h->fp8 ? split_workspace(h->E, 2 * (int)h->H, h->num_sms) : 0;
     for (size_t s : {s1, s2}) parts = s > parts ? s : parts;
+  } else if (h->gated) {
+    parts = glu_f32_workspace(h->num_sms);
   }
   R.err = c.take<unsigned>(1 + h->nfcount);     // the error word, then the arrival counts
   h->fcount = R.err ? R.err + 1 : nullptr;

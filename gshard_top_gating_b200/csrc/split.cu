@@ -13,8 +13,9 @@ namespace moe {
 
 namespace {
 
-// 8 columns per thread; block (x, y): a row of expert y and 2048 of its columns at a time.
-__global__ void __launch_bounds__(256) split_join_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ y,
+// 8 columns per thread, experts in grid.y.
+template <typename T>
+__global__ void __launch_bounds__(256) split_join_kernel(const float* __restrict__ part, T* __restrict__ y,
                                                          const int32_t* __restrict__ nexp, int rows, int64_t C, int N,
                                                          int splits) {
   pdl_wait();
@@ -39,8 +40,14 @@ __global__ void __launch_bounds__(256) split_join_kernel(const float* __restrict
       s[6] += b.z;
       s[7] += b.w;
     }
-    *reinterpret_cast<uint4*>(y + ((int64_t)e * C + r) * N + c) =
-        make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+    T* out = y + ((int64_t)e * C + r) * N + c;
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4*>(out) =
+          make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+    } else {
+      reinterpret_cast<float4*>(out)[0] = make_float4(s[0], s[1], s[2], s[3]);
+      reinterpret_cast<float4*>(out)[1] = make_float4(s[4], s[5], s[6], s[7]);
+    }
   }
 }
 
@@ -69,11 +76,22 @@ size_t split_workspace(int E, int N, int num_sms) {
   return (int64_t)E * ((N + 255) / 256) * 2 <= num_sms / 2 ? (size_t)(num_sms / 2) * 256 * 256 : 0;
 }
 
-cudaError_t split_join(const float* part, void* y, const int32_t* n, int E, int64_t rows, int64_t C, int N, int splits,
-                       cudaStream_t st) {
+namespace {
+
+template <typename T>
+cudaError_t launch_join(const float* part, T* y, const int32_t* n, int E, int64_t rows, int64_t C, int N, int splits,
+                        cudaStream_t st) {
   const int64_t work = (rows * (N / 8) + 255) / 256, most = (148 * 8 + E - 1) / E;
-  return launch_pdl(split_join_kernel, dim3((unsigned)(work < most ? work : most), E), dim3(256), 0, st, part,
-                    static_cast<__nv_bfloat16*>(y), n, (int)rows, C, N, splits);
+  return launch_pdl(split_join_kernel<T>, dim3((unsigned)(work < most ? work : most), E), dim3(256), 0, st, part, y, n,
+                    (int)rows, C, N, splits);
+}
+
+}  // namespace
+
+cudaError_t split_join(const float* part, void* y, bool bf16, const int32_t* n, int E, int64_t rows, int64_t C, int N,
+                       int splits, cudaStream_t st) {
+  if (bf16) return launch_join(part, static_cast<__nv_bfloat16*>(y), n, E, rows, C, N, splits, st);
+  return launch_join(part, static_cast<float*>(y), n, E, rows, C, N, splits, st);
 }
 
 }  // namespace moe

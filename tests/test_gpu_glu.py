@@ -132,6 +132,7 @@ CASES = [
     (2, 128, 192, 1216, [128, 33]),
     (1, 333, 320, 2048, [333]),                                  # few tiles: the depth is cut into shares
     (2, 100, 192, 1216, [100, 33]),
+    (1, 3, 64, 2944, [3]),
     (12, 700, 192, 320, [160, 161, 256, 257, 288, 289, 416, 417, 511, 512, 544, 700]),   # last tiles of 1 to 256 rows
     (32, 18, 512, 1024, [(7 * i) % 19 for i in range(32)]),      # long shares: part of the work is fetched
 ]
