@@ -1,6 +1,6 @@
 // glu_api.cu -- the C ABI of gated experts (moe_glu_* of include/moe.h): handle, workspace,
-// launch sequence.  Forward: up, down.  Backward: the tail copies of x and dy, dW2, dh,
-// dW13, dx.
+// launch sequence.  Forward: up, down.  Backward: dh (which copies the tails of x and dy too),
+// dW2 and dW13, dx.
 #include <new>
 
 #include "api_util.h"
@@ -212,10 +212,8 @@ moe_status moe_glu_backward(moe_glu_handle h, int64_t C, const void* x, const in
   a.dW2 = dW2;
   a.skip_empty = (flags & MOE_BWD_SKIP_EMPTY_EXPERTS) != 0;
   if (h->act == MOE_BF16) {
-    GLU_TRY(glu_tail_bf16(a));
-    GLU_TRY(glu_dw2_bf16(a));
     GLU_TRY(glu_dh_bf16(a));
-    GLU_TRY(glu_dw13_bf16(a));
+    GLU_TRY(glu_dw_bf16(a));
     GLU_TRY(glu_dx_bf16(a));
   } else {
     GLU_TRY(glu_dw2_f32(a));

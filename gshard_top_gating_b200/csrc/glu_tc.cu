@@ -69,19 +69,36 @@ static_assert(smem_bytes(kUp) + 81 * 1024 > 228 * 1024 && smem_bytes(kUpSave) + 
 struct PairArgs {
   const int32_t* n;      // [E] rows per expert, clamped to [0, C]
   int E, C;
-  int64_t Ca, Cb, Cd;    // rows per expert of A, of B (kDw) and of the output
-  int K, N;              // depth (kDw: unused) and output columns (kUp: H; kDw: Q)
-  int P;                 // kDw: output rows per expert
-  int tailA, tailB;      // kDw: the last, partial 64-row block comes from the tail maps
-  int store_zero;        // kDw: experts without rows get zeros (else keep what they hold)
+  int64_t Ca, Cd;        // rows per expert of A and of the output
+  int K, N;              // depth and output columns (kUp: H)
   __nv_bfloat16* D;      // output, for the row-by-row stores (kDown, kDx)
   int splits, rows;      // kDown, kDx: shares of the depth (split.cu); most rows an expert holds
   float* part;           // splits > 1: [splits][E, rows, N] fp32 sums instead of D
+  const uint4 *x, *dy;   // kDh, if tx: the rows whose last, partial blocks go to tx and tdy
+  uint4 *tx, *tdy;
   unsigned* err;
   uint64_t limit_ns;
 };
 
-__device__ __forceinline__ int rows_of(const PairArgs& a, int e) { return min(max(a.n[e], 0), a.C); }
+// One weight gradient, D[e] = A[e, :n]^T B[e, :n] ([P, Q] per expert).
+struct DwProduct {
+  CUtensorMap tmA, tmB, tmD, tmAt, tmBt;
+  int64_t Ca, Cb;        // rows per expert of A and of B
+  int P, Q;
+  int tailA, tailB;      // the last, partial 64-row block comes from the tail maps
+};
+struct DwArgs {
+  DwProduct d[2];
+  int products;          // 1 or 2, the tiles of d[1] after those of d[0]
+  const int32_t* n;
+  int E, C;
+  int store_zero;        // experts without rows get zeros (else keep what they hold)
+  unsigned* err;
+  uint64_t limit_ns;
+};
+
+template <typename A>
+__device__ __forceinline__ int rows_of(const A& a, int e) { return min(max(a.n[e], 0), a.C); }
 
 // idesc: kind::f16, D fp32, A and B bf16, M = 256, N = 256; a_mn / b_mn: operand's rows or
 // columns contiguous instead of its depth.
@@ -228,6 +245,26 @@ __device__ __forceinline__ void load_gu(const CUtensorMap* tmGU, uint32_t tile, 
 }
 
 // MODE kUp, kUpSave, kDown, kDh, kDx.  tmD2: kUpSave the [g|u] output, kDh the [g|u] input.
+// The last, partial block of 64 rows of each expert of x and dy, zero-filled, to tx and tdy:
+// what the weight gradients read instead of the caller's rows past the last one.  Warp `gw` of
+// `warps` takes pieces of 128 x 16 bytes.
+__device__ __forceinline__ void copy_tails(const PairArgs& a, const int* nrows, int gw, int warps, int lane) {
+  const int row16 = a.K / 8;             // dh's depth is M, the rows' width: a multiple of 64
+  const int per = BK * row16 / 128, total = 2 * a.E * per;
+  for (int c = gw; c < total; c += warps) {
+    const int b = c / per, e = b >> 1, at = (c - b * per) * 128 + lane;
+    const int n = nrows[e], rem = n & (BK - 1);
+    if (rem == 0) continue;
+    const uint4* src = (b & 1 ? a.dy : a.x) + (e * a.Ca + n - rem) * row16;
+    uint4* dst = (b & 1 ? a.tdy : a.tx) + (int64_t)e * BK * row16;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = at + 32 * j < rem * row16 ? src[at + 32 * j] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[at + 32 * j] = v[j];
+  }
+}
+
 template <int MODE, int FN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     glu_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -423,6 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, i = 0;
     uint32_t gph = 0;            // kDh: phase bits of the two (g, u) buffers
+    if (MODE == kDh && a.tx)     // while the first tile's products run
+      copy_tails(a, nrows, blockIdx.x * epi_warps(MODE) + warp - 2, gridDim.x * epi_warps(MODE), lane);
     for (int tile = pair; it.decode(tile_of(tile), e, mt, nt); tile += npairs, ++i) {
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1;
@@ -536,13 +575,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
   }
 }
 
-// Weight gradients D[e] = A[e, :n]^T B[e, :n] ([P, N] per expert): both operands with their
-// rows as the depth.  Rows n .. ceil64(n) - 1 of an operand hold zeros, or its last, partial
-// block is read from a tail copy ([E, 64, width], zero-filled; tailA / tailB).
+// Weight gradients D[e] = A[e, :n]^T B[e, :n]: both operands with their rows as the depth.
+// Rows n .. ceil64(n) - 1 of an operand hold zeros, or its last, partial block is read from a
+// tail copy ([E, 64, width], zero-filled; tailA / tailB).  dW2 and dW13 go as one launch, so
+// that the second's tiles fill the first's last wave and a step has a launch less: MERGE.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
-    glu_dw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmAt,
-                  const __grid_constant__ CUtensorMap tmBt, const PairArgs a) {
+    glu_dw_kernel(const __grid_constant__ DwArgs a) {
   constexpr int STAGES = stages(kDw);
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -564,8 +602,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int PT = (a.P + PM - 1) / PM, QT = (a.N + PN - 1) / PN;
-  const int per_e = PT * QT, total = a.E * per_e;
+  const int QT0 = (a.d[0].Q + PN - 1) / PN, QT1 = (a.d[1].Q + PN - 1) / PN;
+  const int per0 = (a.d[0].P + PM - 1) / PM * QT0, per1 = (a.d[1].P + PM - 1) / PM * QT1;
+  const int first1 = a.E * per0, total = first1 + (a.products > 1 ? a.E * per1 : 0);
+  // item -> product, expert and tile
+  auto decode = [&](int item, int& e, int& pt, int& qt) -> const DwProduct& {
+    const bool second = item >= first1;
+    const int tile = second ? item - first1 : item, per = second ? per1 : per0, QT = second ? QT1 : QT0;
+    e = tile / per;
+    const int r = tile - e * per;
+    pt = r / QT;
+    qt = r - pt * QT;
+    return a.d[second];
+  };
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -579,8 +628,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&a.d[0].tmA);
+    tma_prefetch_desc(&a.d[0].tmB);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32((const void*)tmem_slot), TMEM_COLS);
@@ -601,8 +650,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < total; tile += npairs) {
-        const int e = tile / per_e, r = tile - e * per_e;
-        const int pt = r / QT, qt = r - pt * QT;
+        int e, pt, qt;
+        const DwProduct& d = decode(tile, e, pt, qt);
         const int KB = (nrows[e] + BK - 1) / BK;
         const bool part = (nrows[e] % BK) != 0;
         const int colA = pt * PM + (int)rank * 128, colB = qt * PN + (int)rank * 128;
@@ -616,15 +665,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
           const uint32_t fb = full_bar(s) & kPeerBitMask;
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
           const bool last = part && kb == KB - 1;
-          const bool ta = last && a.tailA, tb = last && a.tailB;
-          const int rowA = ta ? e * BK : (int)(e * a.Ca) + kb * BK;
-          const int rowB = tb ? e * BK : (int)(e * a.Cb) + kb * BK;
-          // columns past P or N (a last tile cut short) read as zeros
+          const bool ta = last && d.tailA, tb = last && d.tailB;
+          const int rowA = ta ? e * BK : (int)(e * d.Ca) + kb * BK;
+          const int rowB = tb ? e * BK : (int)(e * d.Cb) + kb * BK;
+          // columns past P or Q (a last tile cut short) read as zeros
 #pragma unroll
-          for (int j = 0; j < 2; ++j) tma_load_2d_pair(sa + j * 8192u, ta ? &tmAt : &tmA, fb, colA + j * 64, rowA);
+          for (int j = 0; j < 2; ++j) tma_load_2d_pair(sa + j * 8192u, ta ? &d.tmAt : &d.tmA, fb, colA + j * 64, rowA);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            tma_load_2d_pair(sa + A_BYTES + j * 8192u, tb ? &tmBt : &tmB, fb, colB + j * 64, rowB);
+            tma_load_2d_pair(sa + A_BYTES + j * 8192u, tb ? &d.tmBt : &d.tmB, fb, colB + j * 64, rowB);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
@@ -641,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
       bool ok = true;
       int i = 0;
       for (int tile = pair; ok && tile < total; tile += npairs) {
-        const int KB = (nrows[tile / per_e] + BK - 1) / BK;
+        const int KB = (nrows[tile >= first1 ? (tile - first1) / per1 : tile / per0] + BK - 1) / BK;
         if (KB == 0) continue;                  // zero tile: the epilogues store zeros
         const int acc = i & 1;
         const uint32_t aph = (i >> 1) & 1;
@@ -687,8 +736,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     const uint32_t tile0 = tiles0 + (warp - 2) * TILE_BYTES;
     int i = 0;
     for (int tile = pair; tile < total; tile += npairs) {
-      const int e = tile / per_e, r = tile - e * per_e;
-      const int pt = r / QT, qt = r - pt * QT;
+      int e, pt, qt;
+      const DwProduct& d = decode(tile, e, pt, qt);
       const bool zero = nrows[e] == 0;
       const int prow = pt * PM + (int)rank * 128 + q * 32;     // P is a multiple of 64: 32 rows or none
       int acc = 0;
@@ -702,9 +751,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
         }
         tc_fence_after();
       }
-      if (prow < a.P && (!zero || a.store_zero))
-        store_plain(&tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN, tile0, (int64_t)e * a.P + prow, qt * PN, a.N,
-                    32, zero, nullptr, lane);
+      if (prow < d.P && (!zero || a.store_zero))
+        store_plain(&d.tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN, tile0, (int64_t)e * d.P + prow, qt * PN,
+                    d.Q, 32, zero, nullptr, lane);
       if (!zero) {
         tc_fence_before();
         __syncwarp();
@@ -725,24 +774,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
-}
-
-// The last, partial block of 64 rows of each expert of up to two row buffers, zero-filled:
-// what the weight gradients read instead of the caller's rows past the last one.
-__global__ void __launch_bounds__(256) glu_tail_kernel(const uint4* __restrict__ x0, const uint4* __restrict__ x1,
-                                                       uint4* __restrict__ t0, uint4* __restrict__ t1,
-                                                       const int32_t* __restrict__ nexp, int64_t C, int row16) {
-  pdl_wait();
-  const int e = blockIdx.x;
-  const int n = min(max(nexp[e], 0), (int)C);
-  const int first = n & ~(BK - 1), rem = n - first;
-  if (rem == 0) return;
-  const uint4* x = blockIdx.z ? x1 : x0;
-  uint4* t = (blockIdx.z ? t1 : t0) + (int64_t)e * BK * row16;
-  const uint4* src = x + ((int64_t)e * C + first) * row16;
-  const int live = rem * row16, all = BK * row16;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < all; i += gridDim.y * 256)
-    t[i] = i < live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <int MODE, int FN>
@@ -788,26 +819,41 @@ cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB, const C
 
 uint64_t rows(int E, int64_t per) { return (uint64_t)E * (uint64_t)per; }
 
-cudaError_t launch_dw(const GluArgs& a, const void* A, int64_t Ca, int P, const void* At, const void* B, int64_t Cb, int Q,
-                      const void* Bt, void* D) {
-  CUtensorMap tmA, tmB, tmD, tmAt, tmBt;
-  if (!encode_2d(&tmA, A, P, rows(a.E, Ca), 64, BK) || !encode_2d(&tmB, B, Q, rows(a.E, Cb), 64, BK) ||
-      !encode_2d(&tmD, D, Q, rows(a.E, P), 64, 32) ||
-      !encode_2d(&tmAt, At ? At : A, P, At ? rows(a.E, BK) : rows(a.E, Ca), 64, BK) ||
-      !encode_2d(&tmBt, Bt ? Bt : B, Q, Bt ? rows(a.E, BK) : rows(a.E, Cb), 64, BK))
-    return cudaErrorInvalidValue;
-  PairArgs p = pair_args(a);
-  p.Ca = Ca;
-  p.Cb = Cb;
-  p.P = P;
-  p.N = Q;
-  p.tailA = At != nullptr;
-  p.tailB = Bt != nullptr;
-  p.store_zero = !a.skip_empty;
+bool dw_product(DwProduct* d, const GluArgs& a, const void* A, int64_t Ca, int P, const void* At, const void* B, int64_t Cb,
+                int Q, const void* Bt, void* D) {
+  d->Ca = Ca;
+  d->Cb = Cb;
+  d->P = P;
+  d->Q = Q;
+  d->tailA = At != nullptr;
+  d->tailB = Bt != nullptr;
+  return encode_2d(&d->tmA, A, P, rows(a.E, Ca), 64, BK) && encode_2d(&d->tmB, B, Q, rows(a.E, Cb), 64, BK) &&
+         encode_2d(&d->tmD, D, Q, rows(a.E, P), 64, 32) &&
+         encode_2d(&d->tmAt, At ? At : A, P, At ? rows(a.E, BK) : rows(a.E, Ca), 64, BK) &&
+         encode_2d(&d->tmBt, Bt ? Bt : B, Q, Bt ? rows(a.E, BK) : rows(a.E, Cb), 64, BK);
+}
+
+bool dw2_product(DwProduct* d, const GluArgs& a) {
+  return dw_product(d, a, a.h, a.Cp, a.H, nullptr, a.dy, a.C, a.M, a.tdy, a.dW2);
+}
+
+bool dw13_product(DwProduct* d, const GluArgs& a) {
+  return dw_product(d, a, a.x, a.C, a.M, a.tx, a.dgu, a.Cp, 2 * a.H, nullptr, a.dW13);
+}
+
+cudaError_t launch_dw(const GluArgs& a, DwArgs& g, int products) {
+  g.products = products;
+  if (products == 1) g.d[1] = g.d[0];
+  g.n = a.n;
+  g.E = a.E;
+  g.C = (int)a.rows;      // no expert holds more
+  g.store_zero = !a.skip_empty;
+  g.err = a.err;
+  g.limit_ns = a.limit_ns;
   const size_t smem = smem_bytes(kDw);
   cudaError_t e = cudaFuncSetAttribute(glu_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(threads(kDw)), smem, a.st, tmA, tmB, tmD, tmAt, tmBt, p);
+  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(threads(kDw)), smem, a.st, g);
 }
 
 }  // namespace
@@ -841,13 +887,6 @@ cudaError_t glu_down_bf16(const GluArgs& a) {
   return launch_split<kDown>(tmA, tmB, tmD, p, a, a.y);
 }
 
-cudaError_t glu_tail_bf16(const GluArgs& a) {
-  const int row16 = a.M / 8;
-  return launch_pdl(glu_tail_kernel, dim3(a.E, (BK * row16 + 1023) / 1024, 2), dim3(256), 0, a.st,
-                    static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.dy), static_cast<uint4*>(a.tx),
-                    static_cast<uint4*>(a.tdy), a.n, a.C, row16);
-}
-
 cudaError_t glu_dh_bf16(const GluArgs& a) {
   CUtensorMap tmA, tmB, tmD, tmG;
   if (!encode_2d(&tmA, a.dy, a.M, rows(a.E, a.C), BK, 128) ||
@@ -860,6 +899,10 @@ cudaError_t glu_dh_bf16(const GluArgs& a) {
   p.Cd = a.Cp;
   p.K = a.M;
   p.N = a.H;
+  p.x = static_cast<const uint4*>(a.x);
+  p.dy = static_cast<const uint4*>(a.dy);
+  p.tx = static_cast<uint4*>(a.tx);
+  p.tdy = static_cast<uint4*>(a.tdy);
   return launch_fn<kDh>(tmA, tmB, tmD, tmG, p, a);
 }
 
@@ -878,12 +921,20 @@ cudaError_t glu_dx_bf16(const GluArgs& a) {
   return launch_split<kDx>(tmA, tmB, tmD, p, a, a.dx);
 }
 
+cudaError_t glu_dw_bf16(const GluArgs& a) {
+  DwArgs g;
+  if (!dw13_product(&g.d[0], a) || !dw2_product(&g.d[1], a)) return cudaErrorInvalidValue;
+  return launch_dw(a, g, 2);
+}
+
 cudaError_t glu_dw2_bf16(const GluArgs& a) {
-  return launch_dw(a, a.h, a.Cp, a.H, nullptr, a.dy, a.C, a.M, a.tdy, a.dW2);
+  DwArgs g;
+  return dw2_product(&g.d[0], a) ? launch_dw(a, g, 1) : cudaErrorInvalidValue;
 }
 
 cudaError_t glu_dw13_bf16(const GluArgs& a) {
-  return launch_dw(a, a.x, a.C, a.M, a.tx, a.dgu, a.Cp, 2 * a.H, nullptr, a.dW13);
+  DwArgs g;
+  return dw13_product(&g.d[0], a) ? launch_dw(a, g, 1) : cudaErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -296,10 +296,10 @@ cudaError_t glu_up(const GluArgs& a, bool bf16);      // h (and gu)
 cudaError_t glu_down(const GluArgs& a, bool bf16);    // y
 cudaError_t glu_up_bf16(const GluArgs& a);
 cudaError_t glu_down_bf16(const GluArgs& a);
-cudaError_t glu_tail_bf16(const GluArgs& a);    // tx, tdy
-cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu
+cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu; tx, tdy
 cudaError_t glu_dx_bf16(const GluArgs& a);      // dx
-cudaError_t glu_dw2_bf16(const GluArgs& a);
+cudaError_t glu_dw_bf16(const GluArgs& a);      // dW13 and dW2, after dh
+cudaError_t glu_dw2_bf16(const GluArgs& a);     // one of them, where the stages are timed apart
 cudaError_t glu_dw13_bf16(const GluArgs& a);
 size_t glu_f32_workspace(int num_sms);          // floats of partial sums (GluArgs::part)
 cudaError_t glu_up_f32(const GluArgs& a);

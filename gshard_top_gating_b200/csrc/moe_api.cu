@@ -976,12 +976,14 @@ moe_status moe_backward(moe_handle h, int64_t S, const void* x, const void* dy, 
       const int widths[2] = {M, M};
       MOE_TRY(launch_pad_zero(bufs, widths, 2, true, E, h->Cbuf, R, st));
     }
+    // bf16: both weight gradients are one launch, unless each stage has its time measured
+    const bool one = bf16 && !prof;
     MOE_TRY(mark(2));
-    MOE_TRY(bf16 ? glu_dw2_bf16(g) : glu_dw2_f32(g));
+    if (!one) MOE_TRY(bf16 ? glu_dw2_bf16(g) : glu_dw2_f32(g));
     MOE_TRY(mark(3));
     MOE_TRY(bf16 ? glu_dh_bf16(g) : glu_dh_f32(g));
     MOE_TRY(mark(4));
-    MOE_TRY(bf16 ? glu_dw13_bf16(g) : glu_dw13_f32(g));
+    MOE_TRY(one ? glu_dw_bf16(g) : bf16 ? glu_dw13_bf16(g) : glu_dw13_f32(g));
     MOE_TRY(mark(5));
     MOE_TRY(bf16 ? glu_dx_bf16(g) : glu_dx_f32(g));
   } else if (bf16) {
