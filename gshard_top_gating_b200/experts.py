@@ -100,19 +100,21 @@ class GatedExperts:
         C = self._rows("x", x)
         self._rows("dy", dy, C)
         check_tensor("counts", counts, (self.E,), torch.int32, self.device)
-        out = dict(out or {})
-        shapes = {"dx": tuple(x.shape), "dW13": tuple(self._keep[0].shape), "dW2": tuple(self._keep[1].shape)}
-        for name, shape in shapes.items():
-            if out.get(name) is not None:
-                check_tensor(name, out[name], shape, self.act, self.device)
+        out = out or {}
+        dx, dW13, dW2 = out.get("dx"), out.get("dW13"), out.get("dW2")
+        W13, W2 = self._keep
+        for name, t, like in (("dx", dx, x), ("dW13", dW13, W13), ("dW2", dW2, W2)):
+            if t is not None:
+                check_tensor(name, t, like.shape, self.act, self.device)
 
         def call(st):
-            g = {n: out[n] if out.get(n) is not None else torch.empty(s, dtype=self.act, device=self.device)
-                 for n, s in shapes.items()}
+            g = {"dx": torch.empty_like(x) if dx is None else dx,
+                 "dW13": torch.empty_like(W13) if dW13 is None else dW13,
+                 "dW2": torch.empty_like(W2) if dW2 is None else dW2}
             L.moe_glu_backward(self.h, C, x, counts, dy, g["dx"], g["dW13"], g["dW2"],
                                L.MOE_BWD_SKIP_EMPTY_EXPERTS if skip_empty_experts else 0, st)
             return g
-        return launch_on(self.device, stream, (x, counts, dy, *out.values()), call)
+        return launch_on(self.device, stream, (x, counts, dy, dx, dW13, dW2), call)
 
     def check(self, stream=None) -> None:
         """Synchronise and raise a pending device error of this handle."""
