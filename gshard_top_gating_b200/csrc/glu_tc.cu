@@ -17,14 +17,14 @@
 // The caller's rows (x, y, dy, dx) are [E, C, width] with any C; rows at or past n are
 // neither read as data nor written.  Whole 32-row groups leave by TMA; the last group of an
 // expert is stored row by row.  The internal rows (h, [g|u], [dg|du]) are [E, Cp, width]
-// with Cp a multiple of 256, and the rows of an expert's last tile past n are stored as
+// with Cp a multiple of 256, and an expert's rows past n up to a multiple of 64 are stored as
 // zeros in training, since the weight gradients reduce over whole blocks of 64 rows.
 //
 // Roles per CTA: warp 0 loads (TMA), warp 1 issues MMAs (the pair's first CTA) and owns TMEM,
-// warps 2..5 drain the accumulator, double buffered, while the next tile's products run; in
-// `up` and `dh`, whose epilogues evaluate f (and f') and move more tiles, warps 2..9, half of
-// the columns each (with four warps `dh` outlasted its products, 545 against 346 us for
-// 8 x 2048 rows, M = 2048, H = 8192, and `up` did for small M).  Every wait is bounded.
+// warps 2..5 drain the accumulator, double buffered, while the next tile's products run; but
+// in `up`, `dh` and, for few rows, `dW`, warps 2..9, half of the columns each.  With four warps
+// `dh` outlasted its products (545 against 346 us for 8 x 2048 rows, M = 2048, H = 8192), as did
+// `up` for small M.  Every wait is bounded.
 #include "common.cuh"
 #include "glu.cuh"
 #include "internal.h"
@@ -36,7 +36,8 @@ namespace {
 
 constexpr int BK = 64;                 // depth of a stage
 constexpr int PM = 256, PN = 256;      // pair tile
-constexpr int epi_warps(int mode) { return mode == 0 || mode == 1 || mode == 3 ? 8 : 4; }     // kUp, kUpSave, kDh: 8
+enum { kUp = 0, kUpSave = 1, kDown = 2, kDh = 3, kDx = 4, kDw = 5, kDwFew = 6 };
+constexpr int epi_warps(int mode) { return mode == kDown || mode == kDx || mode == kDw ? 4 : 8; }
 constexpr int threads(int mode) { return 64 + 32 * epi_warps(mode); }
 constexpr uint32_t A_BYTES = 128 * BK * 2;            // 16 KB: 128 rows of A
 constexpr uint32_t B_BYTES = 128 * BK * 2;            // 16 KB: 128 columns of B
@@ -44,8 +45,6 @@ constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;   // per CTA
 constexpr uint32_t TMEM_COLS = 2 * PN;                // double-buffered accumulator
 constexpr uint32_t TILE_BYTES = 4096;                 // a 32-row x 64-column bf16 store tile
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;        // shared::cluster address -> the pair's first CTA
-
-enum { kUp = 0, kUpSave = 1, kDown = 2, kDh = 3, kDx = 4, kDw = 5 };
 
 // Shared memory of an epilogue warp: tiles of 32 rows x 32 columns for h; for h, g and u; two
 // buffers of them for g and u, which dg and du leave through; else one of 32 x 64.
@@ -56,15 +55,14 @@ constexpr uint32_t epi_bytes(int mode) {
 constexpr int stages(int mode) { return mode == kUpSave ? 5 : mode == kDh ? 4 : 6; }
 constexpr uint32_t kBars = 512;
 constexpr size_t smem_bytes(int mode) {
-  // alignment slack, stages, store tiles, barriers, misc, tile tables
+  // alignment slack, stages, store tiles, barriers, misc, tile tables (kDw: the counts alone)
   return 1024 + (size_t)stages(mode) * STAGE_BYTES + epi_warps(mode) * epi_bytes(mode) + kBars + 16 +
-         4 * (3 * kMaxExperts + 1);
+         4 * (mode >= kDw ? kMaxExperts : 3 * kMaxExperts + 1);
 }
 // A CTA owns its SM (see the expert GEMMs of ffn_tc.cu): no other TMEM user fits beside it.
-static_assert(smem_bytes(kUp) <= 227 * 1024 && smem_bytes(kUpSave) <= 227 * 1024 &&
-              smem_bytes(kDh) <= 227 * 1024, "shared memory per CTA");
-static_assert(smem_bytes(kUp) + 81 * 1024 > 228 * 1024 && smem_bytes(kUpSave) + 81 * 1024 > 228 * 1024 &&
-              smem_bytes(kDh) + 81 * 1024 > 228 * 1024, "a CTA must own its SM");
+constexpr bool owns_sm(int mode) { return smem_bytes(mode) <= 227 * 1024 && smem_bytes(mode) + 81 * 1024 > 228 * 1024; }
+static_assert(owns_sm(kUp) && owns_sm(kUpSave) && owns_sm(kDown) && owns_sm(kDh) && owns_sm(kDw) && owns_sm(kDwFew),
+              "shared memory per CTA");
 
 struct PairArgs {
   const int32_t* n;      // [E] rows per expert, clamped to [0, C]
@@ -115,12 +113,13 @@ __device__ __forceinline__ void put_half(uint32_t tile, int lane, int half, cons
     st_shared_v4(tile + lane * 128 + (((half * 4 + j) ^ (lane & 7)) << 4), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
                  pk[4 * j + 3]);
 }
-// Plain output of one warp: 32 rows x 256 columns from column col0 (N columns, a multiple
+// Plain output of one warp: 32 rows x WIDTH columns from column col0 (N columns, a multiple
 // of 64), nvalid of the rows kept (and row stores where that is fewer than 32).
+template <int WIDTH>
 __device__ __forceinline__ void store_plain(const CUtensorMap* tmD, uint32_t tmem, uint32_t tile, int64_t row0, int col0,
                                             int N, int nvalid, bool zero, __nv_bfloat16* D, int lane) {
 #pragma unroll 1
-  for (int b = 0; b < PN / 64; ++b) {
+  for (int b = 0; b < WIDTH / 64; ++b) {
     const int col = col0 + b * 64;
     if (col >= N) return;
     if (nvalid == 32) {
@@ -486,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
       tc_fence_after();
       const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN;
       if constexpr (UP) {
-        if (MODE == kUpSave || nvalid > 0)
+        if (MODE == kUpSave ? local < ((nrows[e] + BK - 1) & ~(BK - 1)) : nvalid > 0)
           store_up<FN, MODE == kUpSave>(&tmD, &tmD2, tm + part * 64, tile0, (int)row0, col0, a.N, nvalid, lane);
       } else if constexpr (MODE == kDh) {
         bool ok = true;
@@ -529,9 +528,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
               bulk_commit();
             }
           }
-        } else if (nb > 0) {
-          // rows past the last one in this tile: zeros, so that the block that holds it reduces
-          // over nothing else
+        } else if (nb > 0 && local < ((nrows[e] + BK - 1) & ~(BK - 1))) {
+          // rows past the last one, up to a multiple of 64: zeros, so that the block that holds
+          // it reduces over nothing else
           if (lane == 0) bulk_wait_read0();
           __syncwarp();
           const uint32_t z[16] = {};
@@ -553,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
           const int s = depth_of(tile, from, to);
           if (nvalid > 0)
             store_sums(tm, a.part + (((int64_t)s * a.E + e) * a.rows + local + lane) * a.N, col0, a.N, lane < nvalid);
-        } else if (nvalid > 0) store_plain(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
+        } else if (nvalid > 0) store_plain<PN>(&tmD, tm, tile0, row0, col0, a.N, nvalid, false, a.D, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -578,22 +577,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
 // Weight gradients D[e] = A[e, :n]^T B[e, :n]: both operands with their rows as the depth.
 // Rows n .. ceil64(n) - 1 of an operand hold zeros, or its last, partial block is read from a
 // tail copy ([E, 64, width], zero-filled; tailA / tailB).  dW2 and dW13 go as one launch, so
-// that the second's tiles fill the first's last wave and a step has a launch less: MERGE.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
+// that the second's tiles fill the first's last wave and a step has a launch less (3 x 361 rows,
+// M = 64, H = 1664: the step 60 -> 53 us, with the tails copied by `dh`).
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     glu_dw_kernel(const __grid_constant__ DwArgs a) {
-  constexpr int STAGES = stages(kDw);
+  constexpr int STAGES = stages(MODE);
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   unsigned char* gbase = smem_raw + (base - raw_base);
   const uint32_t tiles0 = base + STAGES * STAGE_BYTES;
-  const uint32_t bar0 = tiles0 + 4 * TILE_BYTES;
+  const uint32_t bar0 = tiles0 + epi_warps(MODE) * TILE_BYTES;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
   auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
-  unsigned char* misc = gbase + STAGES * STAGE_BYTES + 4 * TILE_BYTES + kBars;
+  unsigned char* misc = gbase + STAGES * STAGE_BYTES + epi_warps(MODE) * TILE_BYTES + kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   int* nrows = reinterpret_cast<int*>(misc + 16);      // [E]
@@ -623,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 2 * epi_warps(kDw));
+      mbar_init(tempty_bar(i), 2 * epi_warps(MODE));
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -732,7 +733,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    constexpr int WIDTH = PN * 4 / epi_warps(MODE);      // columns of a warp
+    const int q = warp & 3, part = (warp - 2) >> 2;      // its 32 rows, and columns
     const uint32_t tile0 = tiles0 + (warp - 2) * TILE_BYTES;
     int i = 0;
     for (int tile = pair; tile < total; tile += npairs) {
@@ -752,8 +754,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kDw), 1)
         tc_fence_after();
       }
       if (prow < d.P && (!zero || a.store_zero))
-        store_plain(&d.tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN, tile0, (int64_t)e * d.P + prow, qt * PN,
-                    d.Q, 32, zero, nullptr, lane);
+        store_plain<WIDTH>(&d.tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + part * WIDTH, tile0,
+                         (int64_t)e * d.P + prow, qt * PN + part * WIDTH, d.Q, 32, zero, nullptr, lane);
       if (!zero) {
         tc_fence_before();
         __syncwarp();
@@ -850,10 +852,15 @@ cudaError_t launch_dw(const GluArgs& a, DwArgs& g, int products) {
   g.store_zero = !a.skip_empty;
   g.err = a.err;
   g.limit_ns = a.limit_ns;
-  const size_t smem = smem_bytes(kDw);
-  cudaError_t e = cudaFuncSetAttribute(glu_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // Up to 8 blocks of 64 rows a tile's products end before four warps have drained the last one
+  // (2.3 us): eight warps (25 x 18 rows, M = 768, H = 3776: 106 -> 89 us; 683 rows: equal).  Past
+  // that eight cost the products more than they gain (step of 10 x 760 rows: 980 -> 1011 us).
+  const bool few = a.rows <= 8 * BK;
+  auto kern = few ? glu_dw_kernel<kDwFew> : glu_dw_kernel<kDw>;
+  const size_t smem = few ? smem_bytes(kDwFew) : smem_bytes(kDw);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(glu_dw_kernel, dim3(a.num_sms & ~1), dim3(threads(kDw)), smem, a.st, g);
+  return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(few ? threads(kDwFew) : threads(kDw)), smem, a.st, g);
 }
 
 }  // namespace
