@@ -7,7 +7,7 @@
 // acc += (xs ws) * block.  So the tensor cores never accumulate across blocks, and the outer
 // sum is fp32 as well; y is rounded to bf16 once.
 //
-// A CTA pair (cta_group::2) computes 256 rows x 256 columns; CTA r holds rows [128r, +128) of
+// A CTA pair (cta_group::2) computes 256 rows x TN = 256 columns; CTA r holds rows [128r, +128) of
 // xq and columns [128r, +128) of wq, and all 256 columns of its rows in TMEM.  Two TMEM
 // buffers of 256 columns take turns: while the MMAs fill one with block kb + 1, eight warps
 // drain block kb from the other, each thread 128 columns of one row -- one row scale times
@@ -16,6 +16,12 @@
 // handed back as soon as its last column is in registers, by one arrival per warp (the second
 // CTA's arrivals cross to the first).  Rows past the count are neither read as data nor
 // written; every wait is bounded.
+//
+// With fewer tiles than pairs the depth of one tile bounds the product, and the drain of 256
+// columns most of each block: then tiles of 128 or 64 columns, the narrowest that still fit on
+// the pairs at once, a warp draining 64 or 32 (333 x 1456 x 2008: 12.4 -> 9.6 us; 130 rows of 3
+// experts, 2752 x 360: 23.5 -> 13.3).  In a second wave they lose: xq is read for each column
+// of tiles (8 x 256 rows, 1024 x 2048: 10.6 us in tiles of 256 columns, 13.1 in 128).
 #include "common.cuh"
 #include "internal.h"
 #include "tc_tile.cuh"
@@ -25,15 +31,14 @@ namespace moe {
 namespace {
 
 constexpr int BK = 128;                 // depth of a stage = of a scale block (bytes)
-constexpr int PM = 256, PN = 256;
+constexpr int PM = 256;                 // rows of a tile; its columns TN: 256, 128 or 64
 constexpr int kThreads = 384;           // loads, MMAs and two idle warps; eight draining warps
 constexpr int kDrainWarps = 8;
 // Registers: 384 threads launch with 168 each (64,512); 128 keep 40, 256 take 232 (the same).
 constexpr int kRegsLoad = 40, kRegsDrain = 232;
-constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t A_BYTES = 128 * BK, STAGE_BYTES = 2 * A_BYTES;     // A, and up to as much of B
 constexpr int STAGES = 5;
-constexpr double kBlockUs = 0.6;        // 256 x 256 x 128 on a pair, drained
-constexpr uint32_t TMEM_COLS = 2 * PN;
+constexpr double kBlockUs = 0.3;        // 256 x 64 x 128 on a pair, drained
 constexpr uint32_t TILE_BYTES = 4096;   // 32 rows x 64 bf16 columns
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;
 constexpr uint32_t kBars = 256;
@@ -54,10 +59,12 @@ struct Fp8Pair {
   uint64_t limit_ns;
 };
 
-template <bool SPLIT>
+template <bool SPLIT, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmD, const Fp8Pair a) {
+  constexpr uint32_t TMEM_COLS = 2 * TN;
+  constexpr int COLS = TN / 2;                         // columns of a CTA's part of B, and of a draining warp
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;   // same offset in both CTAs
@@ -80,7 +87,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int NT = (a.N + PN - 1) / PN;
+  const int NT = (a.N + TN - 1) / TN;
   const int KB = a.KB, splits = SPLIT ? a.splits : 1;
   // item -> tile, and the item's blocks of depth
   auto tile_of = [&](int item) { return SPLIT ? item / splits : item; };
@@ -151,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int e, mt, nt;
       for (int tile = pair; ok && it.decode(tile_of(tile), e, mt, nt); tile += npairs) {
         const int rowA = e * a.C + mt * PM + (int)rank * 128;
-        const int rowB = e * a.N + nt * PN + (int)rank * 128;
+        const int rowB = e * a.N + nt * TN + (int)rank * COLS;
         int from, to;
         depth_of(tile, from, to);
         for (int kb = from; kb < to; ++kb) {
@@ -162,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const uint32_t sa = base + s * STAGE_BYTES;
           const uint32_t fb = full_bar(s) & kPeerBitMask;
-          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (A_BYTES + COLS * BK));
           // depth past K (a last block cut short) reads as zeros
           tma_load_2d_pair(sa, &tmA, fb, kb * BK, rowA);
           tma_load_2d_pair(sa + A_BYTES, &tmB, fb, kb * BK, rowB);
@@ -178,8 +185,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (lane == 0 && leader) {
       TileIter it{tile_pre, mtiles, a.E, NT, 0};
-      // kind::f8f6f4, D fp32, A and B e4m3 (0) with contiguous depth, M = 256, N = 256
-      const uint32_t idesc = (1u << 4) | ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+      // kind::f8f6f4, D fp32, A and B e4m3 (0) with contiguous depth, M = 256, N = TN
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
@@ -198,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t sa = base + s * STAGE_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            tc_mma_f8_pair(tmem_base + acc * PN, desc_sw128(sa + kk * 32u, 16u, 1024u),
+            tc_mma_f8_pair(tmem_base + acc * TN, desc_sw128(sa + kk * 32u, 16u, 1024u),
                            desc_sw128(sa + A_BYTES + kk * 32u, 16u, 1024u), idesc, kk != 0);
           tc_commit_pair(tfull_bar(acc), 0x3);
           tc_commit_pair(empty_bar(s), 0x3);
@@ -221,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ drain (warps 4..11, both CTAs)
     reg_inc<kRegsDrain>();
     const int q = warp & 3;                        // TMEM lane quarter of this warp
-    const int half = (warp - 4) >> 2;              // its 128 of the tile's 256 columns
+    const int half = (warp - 4) >> 2;              // its half of the tile's columns
     const uint32_t tile0 = tiles0 + (warp - 4) * TILE_BYTES;
     TileIter it{tile_pre, mtiles, a.E, NT, 0};
     int e, mt, nt, acc = 0;
@@ -231,16 +238,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int local = mt * PM + (int)rank * 128 + q * 32;
       const int nvalid = min(32, nrows[e] - local);
       const int64_t row0 = (int64_t)e * a.C + local;
-      const int col0 = nt * PN + half * 128;
-      const int nb = nt * 2 + half;
+      const int col0 = nt * TN + half * COLS;
+      const int nb = col0 >> 7;
       const bool live = lane < nvalid && nb < a.NB;
       const float* xs = a.xs + (row0 + (live ? lane : 0)) * KB;
       const float* ws = a.ws + ((int64_t)e * a.NB + (live ? nb : 0)) * KB;
       int from, to;
       depth_of(tile, from, to);
-      uint64_t sum[64];                          // 128 columns, two per register pair
+      uint64_t sum[COLS / 2];                    // two columns per register pair
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = 0ull;
+      for (int j = 0; j < COLS / 2; ++j) sum[j] = 0ull;
       auto scale = [&](int kb, float& x, float& w) {
         x = live && kb < to ? __ldg(xs + kb) : 0.f;
         w = live && kb < to ? __ldg(ws + kb) : 0.f;
@@ -255,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float f = x * w;
         const uint64_t sc = pack_f32x2(f, f);
         scale(kb + 4, x, w);
-        const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * PN + half * 128;
+        const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + acc * TN + half * COLS;
         // two groups of 32 columns in flight; the last two are on their way while the first two
         // are added, and the buffer is handed back before those are added
         uint32_t r0[32], r1[32];
@@ -265,21 +272,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             sum[c * 16 + j] = fma_f32x2(sc, pack_u32x2(r[2 * j], r[2 * j + 1]), sum[c * 16 + j]);
         };
         tmem_ld_32x32b_x32(tm, r0);            // (rows past the last one: garbage times 0, not stored)
-        tmem_ld_32x32b_x32(tm + 32, r1);
+        if (COLS > 32) tmem_ld_32x32b_x32(tm + 32, r1);
         tmem_ld_wait();
-        add(0, r0);
-        tmem_ld_32x32b_x32(tm + 64, r0);
-        add(1, r1);
-        tmem_ld_32x32b_x32(tm + 96, r1);
-        tmem_ld_wait();
+        if constexpr (COLS == 128) {
+          add(0, r0);
+          tmem_ld_32x32b_x32(tm + 64, r0);
+          add(1, r1);
+          tmem_ld_32x32b_x32(tm + 96, r1);
+          tmem_ld_wait();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (leader) mbar_arrive(tempty_bar(acc));
           else mbar_arrive_peer(mapa_shared(tempty_bar(acc), 0));
         }
-        add(2, r0);
-        add(3, r1);
+        add(COLS == 128 ? 2 : 0, r0);
+        if constexpr (COLS > 32) add(COLS == 128 ? 3 : 1, r1);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
         return true;
@@ -295,33 +304,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok && lane < nvalid) {
           float* p = a.part + (((int64_t)depth_of(tile, from, to) * a.E + e) * a.rows + local + lane) * a.N;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < COLS / 4; ++j)
             if (col0 + j * 4 < a.N)            // N is a multiple of 8
               __stcg(reinterpret_cast<ulonglong2*>(p + col0 + j * 4), make_ulonglong2(sum[2 * j], sum[2 * j + 1]));
         }
       } else if (ok && nvalid > 0) {
+        const bool whole = nvalid == 32 && COLS >= 64;      // by TMA, 64 columns at a time
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < (COLS + 63) / 64; ++b) {
           const int col = col0 + b * 64;
           if (col < a.N) {
-            if (nvalid == 32) {
+            if (whole) {
               if (lane == 0) bulk_wait_read0();
               __syncwarp();
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < (COLS < 64 ? COLS : 64) / 8; ++j) {
               uint32_t pk[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint64_t v = sum[b * 32 + j * 4 + i];
                 pk[i] = pack_bf16x2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
               }
-              if (nvalid == 32)
+              if (whole)
                 st_shared_v4(tile0 + lane * 128 + ((j ^ (lane & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
               else if (lane < nvalid && col + j * 8 < a.N)       // N is a multiple of 8
                 *reinterpret_cast<uint4*>(a.y + (row0 + lane) * a.N + col + j * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-            if (nvalid == 32) {
+            if (whole) {
               fence_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -346,13 +356,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int TN, bool SPLIT>
+cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmD, const Fp8Pair& p, const Fp8Args& a) {
+  CUtensorMap tmB;
+  if (!encode_2d_bytes(&tmB, a.wq, a.K, (uint64_t)a.E * a.N, BK, TN / 2)) return cudaErrorInvalidValue;
+  auto kern = fp8_pair_kernel<SPLIT, TN>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
+}
+
 }  // namespace
 
 cudaError_t fp8_pair(const Fp8Args& a) {
-  CUtensorMap tmA, tmB, tmD;
+  CUtensorMap tmA, tmD;
   const uint64_t rows = (uint64_t)a.E * (uint64_t)a.C;
-  if (!encode_2d_bytes(&tmA, a.xq, a.K, rows, BK, 128) || !encode_2d_bytes(&tmB, a.wq, a.K, (uint64_t)a.E * a.N, BK, 128) ||
-      !encode_2d(&tmD, a.y, a.N, rows, 64, 32))
+  if (!encode_2d_bytes(&tmA, a.xq, a.K, rows, BK, 128) || !encode_2d(&tmD, a.y, a.N, rows, 64, 32))
     return cudaErrorInvalidValue;
   Fp8Pair p{};
   p.n = a.n;
@@ -366,17 +385,19 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   p.xs = a.xs;
   p.ws = a.ws;
   p.y = static_cast<__nv_bfloat16*>(a.y);
-  p.splits = split_count(a.E, a.rows, a.N, p.KB, kBlockUs, a.num_sms);
   p.rows = (int)a.rows;
   p.part = a.part;
   p.err = a.err;
   p.limit_ns = a.limit_ns;
-  auto kern = p.splits > 1 ? fp8_pair_kernel<true> : fp8_pair_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
+  // the narrowest tiles that fit on the pairs at once; only those can be few enough for shares
+  auto tiles = [&](int TN) { return (int64_t)a.E * ((a.rows + PM - 1) / PM) * ((a.N + TN - 1) / TN); };
+  const int pairs = a.num_sms / 2;
+  if (tiles(128) > pairs) return launch<256, false>(tmA, tmD, p, a);
+  if (tiles(64) > pairs) return launch<128, false>(tmA, tmD, p, a);
+  p.splits = split_count(a.E, a.rows, a.N, 64, p.KB, kBlockUs, a.num_sms);
+  if (p.splits == 1) return launch<64, false>(tmA, tmD, p, a);
+  const cudaError_t e = launch<64, true>(tmA, tmD, p, a);
+  return e != cudaSuccess ? e : split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
 }
 
 }  // namespace moe

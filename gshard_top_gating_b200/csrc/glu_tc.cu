@@ -811,7 +811,7 @@ constexpr double kBlockUs = 0.28;      // 256 x 256 x 64 on a pair
 template <int MODE>
 cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, PairArgs p,
                          const GluArgs& a, void* out) {
-  p.splits = split_count(a.E, a.rows, p.N, p.K / BK, kBlockUs, a.num_sms);
+  p.splits = split_count(a.E, a.rows, p.N, PN, p.K / BK, kBlockUs, a.num_sms);
   p.rows = (int)a.rows;
   p.part = a.part;
   const cudaError_t e = launch_pair<MODE, kGluSilu>(tmA, tmB, tmD, tmD, p, a);

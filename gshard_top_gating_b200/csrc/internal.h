@@ -326,12 +326,12 @@ struct Fp8Args {
   int num_sms;
   cudaStream_t st;
 };
-cudaError_t fp8_matmul(const Fp8Args& a);       // few_rows.cu or 256 x 256 tiles
-cudaError_t fp8_pair(const Fp8Args& a);         // 256 x 256 tiles
-// split.cu: into how many shares of the depth (KB blocks of block_us each on a tile) the 256 x 256
+cudaError_t fp8_matmul(const Fp8Args& a);       // few_rows.cu or tiles of 256 rows
+cudaError_t fp8_pair(const Fp8Args& a);         // tiles of 256 x 256, 128 or 64
+// split.cu: into how many shares of the depth (KB blocks of block_us each on a tile) the 256 x TN
 // tiles of a product are cut (1: not at all), the floats of workspace its sums need at most,
 // and the kernel that adds them: part [splits][E, rows, N] -> y [E, C, N].
-int split_count(int E, int64_t rows, int N, int KB, double block_us, int num_sms);
+int split_count(int E, int64_t rows, int N, int TN, int KB, double block_us, int num_sms);
 size_t split_workspace(int E, int N, int num_sms);
 cudaError_t split_join(const float* part, void* y, bool bf16, const int32_t* n, int E, int64_t rows, int64_t C, int N,
                        int splits, cudaStream_t st);

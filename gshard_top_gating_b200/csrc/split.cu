@@ -1,6 +1,7 @@
-// split.cu -- products of 256 x 256 tiles that are too few for the device, cut along the depth:
-// each of `splits` CTA pairs takes a share of a tile's depth and stores its fp32 sums, and one
-// more kernel adds them in order of the depth and rounds to bf16.
+// split.cu -- products of 256-row tiles (fp32: of 32) that are too few for the device, cut
+// along the depth: each of `splits` CTA pairs (blocks) takes a share of a tile's depth and
+// stores its fp32 sums, and one more kernel adds them in order of the depth and rounds to the
+// result's type.
 //
 // It costs that kernel, about 7 us, and the sums' way to memory and back, 0.13 us for every
 // tile of them; it saves depth.  One expert of 256 rows, H = 4096 -> M = 1024, has 4 tiles for
@@ -56,8 +57,8 @@ constexpr double kJoinUs = 7.0, kTileUs = 0.13;     // measured: the kernel; a t
 
 }  // namespace
 
-int split_count(int E, int64_t rows, int N, int KB, double block_us, int num_sms) {
-  const int64_t tiles = (int64_t)E * ((rows + 255) / 256) * ((N + 255) / 256);
+int split_count(int E, int64_t rows, int N, int TN, int KB, double block_us, int num_sms) {
+  const int64_t tiles = (int64_t)E * ((rows + 255) / 256) * ((N + TN - 1) / TN);
   const double sums = (double)E * rows * N / 65536.0;      // full tiles' worth
   int best = 1;
   double gain = 0.0;

@@ -137,6 +137,11 @@ CASES = [
     (1, 333, 4112, 520, [333]),                              # few tiles: the depth is cut into shares
     (2, 130, 3088, 1000, [129, 7]),
     (1, 100, 4096, 512, [100]),
+    (1, 300, 656, 4088, [300]),                              # tiles of 128 columns
+    (3, 200, 384, 3208, [200, 0, 161]),
+    (6, 300, 272, 1640, [300, 32, 257, 64, 0, 96]),          # of 256
+    (1, 160, 7168, 200, [160]),                              # of 64, in shares
+    (5, 260, 528, 328, [256, 260, 32, 96, 40]),              # of 64, more than one block of 256 rows
     (32, 9, 2048, 1544, [i % 10 for i in range(32)]),        # long shares: part of the work is fetched
 ]
 
