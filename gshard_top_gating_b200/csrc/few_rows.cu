@@ -863,6 +863,16 @@ cudaError_t glu_down(const GluArgs& a, bool bf16) {
   return glu_few(a) ? glu_few_down(a) : glu_down_bf16(a);
 }
 
+int glu_down_kernels(const GluArgs& a, bool bf16) {
+  return (bf16 ? (glu_few(a) ? 1 : glu_down_shares_bf16(a)) : glu_down_shares_f32(a)) > 1 ? 2 : 1;
+}
+
+int glu_dx_kernels(const GluArgs& a, bool bf16) {
+  return (bf16 ? glu_dx_shares_bf16(a) : glu_dx_shares_f32(a)) > 1 ? 2 : 1;
+}
+
+int fp8_matmul_kernels(const Fp8Args& a) { return a.rows > kRowsFp8 && fp8_shares(a) > 1 ? 2 : 1; }
+
 cudaError_t fp8_matmul(const Fp8Args& a) { return a.rows <= kRowsFp8 ? fp8_few(a) : fp8_pair(a); }
 
 }  // namespace moe

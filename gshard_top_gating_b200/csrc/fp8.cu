@@ -366,7 +366,13 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmD, const Fp8Pair
   return launch_pdl(kern, dim3(a.num_sms & ~1), dim3(kThreads), SMEM, a.st, tmA, tmB, tmD, p);
 }
 
+int64_t tiles(const Fp8Args& a, int TN) { return (int64_t)a.E * ((a.rows + PM - 1) / PM) * ((a.N + TN - 1) / TN); }
+
 }  // namespace
+
+int fp8_shares(const Fp8Args& a) {
+  return tiles(a, 64) > a.num_sms / 2 ? 1 : split_count(a.E, a.rows, a.N, 64, (a.K + 127) / 128, kBlockUs, a.num_sms);
+}
 
 cudaError_t fp8_pair(const Fp8Args& a) {
   CUtensorMap tmA, tmD;
@@ -390,11 +396,10 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   p.err = a.err;
   p.limit_ns = a.limit_ns;
   // the narrowest tiles that fit on the pairs at once; only those can be few enough for shares
-  auto tiles = [&](int TN) { return (int64_t)a.E * ((a.rows + PM - 1) / PM) * ((a.N + TN - 1) / TN); };
   const int pairs = a.num_sms / 2;
-  if (tiles(128) > pairs) return launch<256, false>(tmA, tmD, p, a);
-  if (tiles(64) > pairs) return launch<128, false>(tmA, tmD, p, a);
-  p.splits = split_count(a.E, a.rows, a.N, 64, p.KB, kBlockUs, a.num_sms);
+  if (tiles(a, 128) > pairs) return launch<256, false>(tmA, tmD, p, a);
+  if (tiles(a, 64) > pairs) return launch<128, false>(tmA, tmD, p, a);
+  p.splits = fp8_shares(a);
   if (p.splits == 1) return launch<64, false>(tmA, tmD, p, a);
   const cudaError_t e = launch<64, true>(tmA, tmD, p, a);
   return e != cudaSuccess ? e : split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);

@@ -259,20 +259,25 @@ cudaError_t launch(const SimtArgs& g, int64_t rows, int cols, int E, int num_sms
 // down and dx where 32 x 32 tiles leave SMs idle over a long depth: in shares of at least 256,
 // joined by one more kernel (one row, M = 64, H = 2944, forward: 38 -> 15 us; 2 x 155 rows, M = 320, H = 4800: 186 -> 139 us).
 constexpr int kShareK = 256;
+int shares_of(const GluArgs& a, int cols, int K) {
+  if (tile_of(a.rows, cols, a.E, a.num_sms) != 32) return 1;
+  const int64_t tiles = (a.rows + 31) / 32 * ((cols + 31) / 32) * a.E, s = 2 * a.num_sms / tiles;
+  const int most = K / kShareK;
+  return s < 2 || most < 2 ? 1 : s < most ? (int)s : most;
+}
+
 template <bool BT>
 cudaError_t launch_shares(SimtArgs g, const GluArgs& a, int K, float* out) {
-  const int64_t tiles = (a.rows + 31) / 32 * ((g.cols + 31) / 32) * a.E;
-  int64_t s = tile_of(a.rows, g.cols, a.E, a.num_sms) == 32 ? 2 * a.num_sms / tiles : 1;
-  if (s > K / kShareK) s = K / kShareK;
-  if (s < 2) return launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
-  g.splits = (int)s;
+  const int s = shares_of(a, g.cols, K);
+  if (s == 1) return launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
+  g.splits = s;
   g.D = a.part;
   g.ldd = g.cols;
   g.d_z = a.rows * g.cols;
   g.s_z = a.E * g.d_z;
   const cudaError_t e = launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
   if (e != cudaSuccess) return e;
-  return split_join(a.part, out, false, a.n, a.E, a.rows, a.C, g.cols, (int)s, a.st);
+  return split_join(a.part, out, false, a.n, a.E, a.rows, a.C, g.cols, s, a.st);
 }
 
 template <bool AT, bool BT, int EPI>
@@ -310,6 +315,9 @@ SimtArgs simt_args(const GluArgs& a, const void* A, int64_t a_z, int lda, const 
 
 // tiles x shares stays within two tiles of 32 x 32 per SM.
 size_t glu_f32_workspace(int num_sms) { return (size_t)2 * num_sms * 32 * 32; }
+
+int glu_down_shares_f32(const GluArgs& a) { return shares_of(a, a.M, a.H); }
+int glu_dx_shares_f32(const GluArgs& a) { return shares_of(a, a.M, 2 * a.H); }
 
 cudaError_t glu_up_f32(const GluArgs& a) {
   const int64_t w = (int64_t)a.M * 2 * a.H;

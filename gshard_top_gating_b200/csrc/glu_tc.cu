@@ -808,10 +808,13 @@ PairArgs pair_args(const GluArgs& a) {
 
 // kDown, kDx: with too few tiles for the device, in shares of the depth.
 constexpr double kBlockUs = 0.28;      // 256 x 256 x 64 on a pair
+int shares_of(const GluArgs& a, int N, int K) {
+  return split_count(a.E, a.rows, N, PN, K / BK, kBlockUs, a.num_sms);
+}
 template <int MODE>
 cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, PairArgs p,
                          const GluArgs& a, void* out) {
-  p.splits = split_count(a.E, a.rows, p.N, PN, p.K / BK, kBlockUs, a.num_sms);
+  p.splits = shares_of(a, p.N, p.K);
   p.rows = (int)a.rows;
   p.part = a.part;
   const cudaError_t e = launch_pair<MODE, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
@@ -864,6 +867,9 @@ cudaError_t launch_dw(const GluArgs& a, DwArgs& g, int products) {
 }
 
 }  // namespace
+
+int glu_down_shares_bf16(const GluArgs& a) { return shares_of(a, a.M, a.H); }
+int glu_dx_shares_bf16(const GluArgs& a) { return shares_of(a, a.M, 2 * a.H); }
 
 cudaError_t glu_up_bf16(const GluArgs& a) {
   CUtensorMap tmA, tmB, tmD, tmD2;

@@ -294,6 +294,12 @@ struct GluArgs {
 };
 cudaError_t glu_up(const GluArgs& a, bool bf16);      // h (and gu)
 cudaError_t glu_down(const GluArgs& a, bool bf16);    // y
+int glu_down_kernels(const GluArgs& a, bool bf16);    // launches of glu_down, of dx
+int glu_dx_kernels(const GluArgs& a, bool bf16);
+int glu_down_shares_bf16(const GluArgs& a);           // into which the depth is cut, likewise
+int glu_dx_shares_bf16(const GluArgs& a);
+int glu_down_shares_f32(const GluArgs& a);
+int glu_dx_shares_f32(const GluArgs& a);
 cudaError_t glu_up_bf16(const GluArgs& a);
 cudaError_t glu_down_bf16(const GluArgs& a);
 cudaError_t glu_dh_bf16(const GluArgs& a);      // dgu; tx, tdy
@@ -327,6 +333,8 @@ struct Fp8Args {
   cudaStream_t st;
 };
 cudaError_t fp8_matmul(const Fp8Args& a);       // few_rows.cu or tiles of 256 rows
+int fp8_matmul_kernels(const Fp8Args& a);       // its launches
+int fp8_shares(const Fp8Args& a);               // of fp8_pair: into which the depth is cut
 cudaError_t fp8_pair(const Fp8Args& a);         // tiles of 256 x 256, 128 or 64
 // split.cu: into how many shares of the depth (KB blocks of block_us each on a tile) the 256 x TN
 // tiles of a product are cut (1: not at all), the floats of workspace its sums need at most,

@@ -327,6 +327,62 @@ moe_status create_layer(moe_handle* out, int64_t S_max, int64_t M, int64_t H, in
 
 }  // namespace
 
+namespace {
+
+GluArgs glu_args(moe_handle h, int64_t S, cudaStream_t st) {
+  GluArgs a{};
+  a.E = h->E;
+  a.M = (int)h->M;
+  a.H = (int)h->H;
+  a.fn = h->fn;
+  a.C = a.Cp = h->Cbuf;
+  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
+  a.rows = C < S ? C : S;
+  a.n = h->R.nexp;
+  a.x = h->xbuf;
+  a.W13 = h->W1;
+  a.W2 = h->W2;
+  a.h = h->hbuf;
+  a.gu = h->bws ? h->gu : nullptr;
+  a.y = h->ybuf;
+  a.dy = h->dybuf;
+  a.dgu = h->dpre;
+  a.dx = h->dybuf;          // dY is no longer needed once dW2 and dh are known
+  a.part = h->fpart;
+  a.count = h->fcount;
+  a.err = h->R.err;
+  a.limit_ns = h->wait_limit_ns;
+  a.num_sms = h->num_sms;
+  a.st = st;
+  return a;
+}
+
+Fp8Args fp8_args(moe_handle h, int64_t S, cudaStream_t st, const void* xq, const float* xs, int K, const void* wq,
+                 const float* ws, int N, void* y) {
+  Fp8Args a{};
+  a.E = h->E;
+  a.K = K;
+  a.N = N;
+  a.C = h->Cbuf;
+  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
+  a.rows = C < S ? C : S;
+  a.n = h->R.nexp;
+  a.xq = xq;
+  a.xs = xs;
+  a.wq = wq;
+  a.ws = ws;
+  a.y = y;
+  a.part = h->fpart;
+  a.count = h->fcount;
+  a.err = h->R.err;
+  a.limit_ns = h->wait_limit_ns;
+  a.num_sms = h->num_sms;
+  a.st = st;
+  return a;
+}
+
+}  // namespace
+
 extern "C" {
 
 const char* moe_status_string(moe_status s) {
@@ -409,6 +465,12 @@ int32_t moe_kernels_per_forward(moe_handle h, int64_t S) {
   if (!h || S <= 0) return 0;
   const bool reroute = (h->route_flags & MOE_ROUTE_REROUTE) != 0;
   int n = (reroute ? 8 : (fuses_combine(h) ? 5 : 6)) + (h->fp8 ? 2 : 0);
+  if (h->fp8) {
+    n += fp8_matmul_kernels(fp8_args(h, S, nullptr, nullptr, nullptr, (int)h->M, nullptr, nullptr, 2 * (int)h->H, nullptr)) +
+         fp8_matmul_kernels(fp8_args(h, S, nullptr, nullptr, nullptr, (int)h->H, nullptr, nullptr, (int)h->M, nullptr)) - 2;
+  } else if (h->gated) {
+    n += glu_down_kernels(glu_args(h, S, nullptr), h->act == MOE_BF16) - 1;
+  }
   if (h->act == MOE_BF16 && kMixedTiles && !h->gated && h->Cbuf % 256 == 0) {
     const int64_t C = capacity_of(h->cf, h->k, S, h->E);
     const bool saturated = (double)S * h->k / h->E >= (double)C;
@@ -452,58 +514,6 @@ struct NvtxStages {
 
 // The gated experts' products on the layer's own buffers (padded with zeros to a multiple of
 // 64 rows where the backward reduces over them, so without tail copies).
-GluArgs glu_args(moe_handle h, int64_t S, cudaStream_t st) {
-  GluArgs a{};
-  a.E = h->E;
-  a.M = (int)h->M;
-  a.H = (int)h->H;
-  a.fn = h->fn;
-  a.C = a.Cp = h->Cbuf;
-  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
-  a.rows = C < S ? C : S;
-  a.n = h->R.nexp;
-  a.x = h->xbuf;
-  a.W13 = h->W1;
-  a.W2 = h->W2;
-  a.h = h->hbuf;
-  a.gu = h->bws ? h->gu : nullptr;
-  a.y = h->ybuf;
-  a.dy = h->dybuf;
-  a.dgu = h->dpre;
-  a.dx = h->dybuf;          // dY is no longer needed once dW2 and dh are known
-  a.part = h->fpart;
-  a.count = h->fcount;
-  a.err = h->R.err;
-  a.limit_ns = h->wait_limit_ns;
-  a.num_sms = h->num_sms;
-  a.st = st;
-  return a;
-}
-
-Fp8Args fp8_args(moe_handle h, int64_t S, cudaStream_t st, const void* xq, const float* xs, int K, const void* wq,
-                 const float* ws, int N, void* y) {
-  Fp8Args a{};
-  a.E = h->E;
-  a.K = K;
-  a.N = N;
-  a.C = h->Cbuf;
-  const int64_t C = capacity_of(h->cf, h->k, S, h->E);
-  a.rows = C < S ? C : S;
-  a.n = h->R.nexp;
-  a.xq = xq;
-  a.xs = xs;
-  a.wq = wq;
-  a.ws = ws;
-  a.y = y;
-  a.part = h->fpart;
-  a.count = h->fcount;
-  a.err = h->R.err;
-  a.limit_ns = h->wait_limit_ns;
-  a.num_sms = h->num_sms;
-  a.st = st;
-  return a;
-}
-
 moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStream_t st) {
   if (!h || S < 0 || S > h->S_max) return MOE_ERR_INVALID_ARG;
   if (S > 0 && (!x || !y || !aligned(x, 16) || !aligned(y, 16))) return MOE_ERR_INVALID_ARG;
@@ -878,7 +888,10 @@ moe_status moe_set_backward_flags(moe_handle h, uint32_t flags) {
 
 int32_t moe_kernels_per_backward(moe_handle h, int64_t S) {
   if (!h || S <= 0) return 0;
-  return h->act == MOE_BF16 ? 10 : 8;
+  const bool bf16 = h->act == MOE_BF16;
+  int n = bf16 ? 10 : 8;
+  if (h->gated) n += glu_dx_kernels(glu_args(h, S, nullptr), bf16) - 1 - (bf16 && !(h->profiling && h->have_events) ? 1 : 0);
+  return n;
 }
 
 moe_status moe_backward(moe_handle h, int64_t S, const void* x, const void* dy, float a_aux, float a_z,

@@ -212,7 +212,7 @@ def test_backward_needs_a_forward_that_kept_g_and_u():
 
 def test_kernels_per_call_and_refusals():
     w, x, Wg, b, W13, W2, layer = build(64, 64, 128, 4, 1, 1.25, "bf16", "silu")
-    assert L.moe_kernels_per_forward(layer.h, 64) == 6 and L.moe_kernels_per_backward(layer.h, 64) == 10
+    assert L.moe_kernels_per_forward(layer.h, 64) == 6 and L.moe_kernels_per_backward(layer.h, 64) == 9
     for bad in ("tanh", "SILU", 3):
         with pytest.raises(ValueError):
             MoeLayer(64, 64, 128, 4, 1, 1.25, Wg, b, W13, W2, activation=bad)
@@ -314,8 +314,26 @@ def test_forward_from_host_memory_and_stage_times():
     L.moe_set_profiling(layer.h, True)
     layer.enable_backward()
     layer(x)
-    layer.backward(x, upstream_grad(w, device="cuda"))
+    grads = layer.backward(x, upstream_grad(w, device="cuda"))
     assert all(t >= 0 for t in L.moe_get_stage_times(layer.h) + L.moe_get_backward_stage_times(layer.h))
+    # with the stages timed the weight gradients are a launch each, with the same results
+    assert L.moe_kernels_per_backward(layer.h, 300) == 10
+    L.moe_set_profiling(layer.h, False)
+    assert L.moe_kernels_per_backward(layer.h, 300) == 9
+    layer(x)
+    for name, t in layer.backward(x, upstream_grad(w, device="cuda")).items():
+        assert t is None or torch.equal(t, grads[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_kernel_counts_where_the_depth_is_cut(dtype):
+    """The layer counts the kernels that join shares."""
+    w, x, Wg, b, W13, W2, layer = build(40, 64, 4096, 1, 1, 1.0, dtype, "silu")
+    assert L.moe_kernels_per_forward(layer.h, 40) == 7
+    assert L.moe_kernels_per_backward(layer.h, 40) == {"f32": 9, "bf16": 10}[dtype]
+    wide = build(40, 64, 4096, 1, 1, 1.0, dtype, "silu", S_max=16384)[-1]
+    assert L.moe_kernels_per_forward(wide.h, 16384) == 6
+    assert L.moe_kernels_per_backward(wide.h, 16384) == {"f32": 8, "bf16": 9}[dtype]
 
 
 def test_two_layers_on_two_streams():
