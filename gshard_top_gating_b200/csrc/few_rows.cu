@@ -69,7 +69,7 @@ struct FewArgs {
   int64_t Cb, Cd;        // rows per expert of the rows' operand and of the output
   int K;                 // rows of a bf16 weight matrix (its depth)
   __nv_bfloat16* D;      // output, N columns
-  __nv_bfloat16* gu;     // kUp: [g|u], 2N columns, or null
+  uint16_t* gu;          // kUp: [g|u], 2N columns (glu.cuh), or null
   const float* xs;       // kFp8: [E, C, KB]
   const float* ws;       // kFp8: [E, NB, KB]
   float* part;           // [(2 + kPieces) * grid][ACC * NT][128] partial sums
@@ -159,8 +159,8 @@ __device__ __forceinline__ void put(const FewArgs& a, int64_t row, int f, const 
     const float h = glu_f<FN, true>(v[0]) * v[1];
     a.D[row * a.N + f] = __float2bfloat16_rn(live ? h : 0.f);
     if (a.gu) {
-      a.gu[row * 2 * a.N + f] = __float2bfloat16_rn(live ? v[0] : 0.f);
-      a.gu[row * 2 * a.N + a.N + f] = __float2bfloat16_rn(live ? v[1] : 0.f);
+      a.gu[row * 2 * a.N + f] = pack_gu_lane(v[0], live);
+      a.gu[row * 2 * a.N + a.N + f] = pack_gu_lane(v[1], live);
     }
   } else {
 #pragma unroll
@@ -778,7 +778,7 @@ cudaError_t glu_few_up(const GluArgs& a) {
   f.Cb = a.C;
   f.Cd = a.Cp;
   f.D = static_cast<__nv_bfloat16*>(a.h);
-  f.gu = static_cast<__nv_bfloat16*>(a.gu);
+  f.gu = static_cast<uint16_t*>(a.gu);
   f.part = a.part;
   f.count = a.count;
   f.err = a.err;

@@ -25,6 +25,8 @@
 // in `up`, `dh` and, for few rows, `dW`, warps 2..9, half of the columns each.  With four warps
 // `dh` outlasted its products (545 against 346 us for 8 x 2048 rows, M = 2048, H = 8192), as did
 // `up` for small M.  Every wait is bounded.
+#include <type_traits>
+
 #include "common.cuh"
 #include "glu.cuh"
 #include "internal.h"
@@ -214,13 +216,9 @@ __device__ __forceinline__ void store_up(const CUtensorMap* tmD, const CUtensorM
     }
     put_narrow(tile, lane, pk);
     if (SAVE) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        pk[j] = live ? pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])) : 0u;
+      pack_gu(g, live, pk);
       put_narrow(tile + NARROW_BYTES, lane, pk);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        pk[j] = live ? pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])) : 0u;
+      pack_gu(u, live, pk);
       put_narrow(tile + 2 * NARROW_BYTES, lane, pk);
     }
     fence_async_smem();
@@ -508,16 +506,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
             get_narrow(buf, lane, pg);
             get_narrow(buf + NARROW_BYTES, lane, pu);
             tmem_ld_wait();
+            const bool fg = gu_is_fine(pg[0]), fu = gu_is_fine(pu[0]), live = lane < nvalid;
+            auto gradients = [&](auto all_fine) {
+              constexpr bool FINE = decltype(all_fine)::value;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float d0 = __uint_as_float(r[2 * j]), d1 = __uint_as_float(r[2 * j + 1]);
-              float f0, df0, f1, df1;
-              glu_f_df<FN, true>(bf16lo(pg[j]), f0, df0);
-              glu_f_df<FN, true>(bf16hi(pg[j]), f1, df1);
-              const float u0 = bf16lo(pu[j]), u1 = bf16hi(pu[j]);
-              pg[j] = lane < nvalid ? pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1) : 0u;
-              pu[j] = lane < nvalid ? pack_bf16x2(d0 * f0, d1 * f1) : 0u;
-            }
+              for (int j = 0; j < 16; ++j) {
+                const float d0 = __uint_as_float(r[2 * j]), d1 = __uint_as_float(r[2 * j + 1]);
+                float g0, g1, u0, u1, f0, df0, f1, df1;
+                unpack_gu<FINE>(pg[j], fg, g0, g1);
+                unpack_gu<FINE>(pu[j], fu, u0, u1);
+                glu_f_df<FN, true>(g0, f0, df0);
+                glu_f_df<FN, true>(g1, f1, df1);
+                pg[j] = live ? pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1) : 0u;
+                pu[j] = live ? pack_bf16x2(d0 * f0, d1 * f1) : 0u;
+              }
+            };
+            if (__all_sync(0xffffffffu, (fg && fu) || !live)) gradients(std::true_type{});
+            else gradients(std::false_type{});
             put_narrow(buf, lane, pg);
             put_narrow(buf + NARROW_BYTES, lane, pu);
             fence_async_smem();

@@ -275,7 +275,7 @@ struct GluArgs {
   const void* W13;       // [E, M, 2H]: Wg in columns [0, H), Wu in [H, 2H)
   const void* W2;        // [E, H, M]
   void* h;               // [E, Cp, H]
-  void* gu;              // [E, Cp, 2H] g and u as the backward reads them, or null (inference)
+  void* gu;              // [E, Cp, 2H] g and u as the backward reads them (bf16: glu.cuh), or null (inference)
   void* y;               // [E, C, M]
   const void* dy;        // [E, C, M]
   void* dgu;             // [E, Cp, 2H]

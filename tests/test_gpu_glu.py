@@ -368,6 +368,32 @@ def test_saturated_gates():
             assert g["dx"].isfinite().all() and g["dW13"].isfinite().all()
 
 
+@pytest.mark.parametrize("fn", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("C", [8, 70], ids=["few rows", "tiles"])
+def test_gradients_of_rows_of_any_magnitude(C, fn):
+    """g and u between the passes hold 16 bits: fp16 for 32 columns that fit it, else bf16,
+    the first of 32 then with a rounding of 2u.  Rows of magnitudes from 1e-9 to 1e9, a row of
+    zeros, and one whose u are past fp16's range in one column in 32 only: dx of each row
+    within the bar of `check` and 1/32 of a rounding more, dW13 of all of them (twice the
+    interval bound, since that first one's error is twice the u it counts)."""
+    M, H = 64, 192
+    x, dy, W13, W2, n = make(1, C, M, H, torch.bfloat16, [C], seed=C)
+    scales = torch.tensor([1.0, 1e-9, 1e9, 1e-5, 3e5, 0.0, 1.0, 300.0], device="cuda").repeat(C // 8 + 1)[:C]
+    x = (x.float() * scales[None, :, None]).bfloat16()
+    W13[0, :, H + 5::32] *= 2.0**14
+    ex = experts(C, W13, W2, fn)
+    ex(x, n)
+    g = ex.backward(x, n, dy)
+    ref = reference(x, dy, W13, W2, n, fn)[0]
+    u = U[torch.bfloat16]
+    bar = (ROUNDINGS["dx"] + 1 / 32) * u
+    val, err, _ = ref["dx"]
+    for i in range(C):
+        slack = float(err[i].norm()) if fn == "relu" else 0.0       # either side of 0 (see check's flips)
+        assert float((g["dx"][0, i].double() - val[i]).norm()) <= bar * float(val[i].norm()) + slack + 1e-30, (i, float(scales[i]))
+    assert bool(((g["dW13"][0].double() - ref["dW13"][0]).abs() <= 2 * ref["dW13"][1] + 1e-30).all())
+
+
 def test_offsets_past_32_bits():
     """x and y of more than 2^31 elements: rows at the far end of both experts."""
     E, C, M, H = 2, 1_060_000, 1024, 64
