@@ -58,6 +58,7 @@ def _load() -> ctypes.CDLL:
         "moe_set_profiling": [P, I32],
         "moe_get_stage_times": [P, ctypes.POINTER(ctypes.c_float), I32],
         "moe_selftest_wait_timeout": [I32, P],
+        "moe_selftest_wait_together": [I32, I32, I32, P],
         "moe_assign_slots_noalloc": [I64, I32, I32, I64, P, P, P, P],
         "moe_enable_backward": [P],
         "moe_set_backward_flags": [P, ctypes.c_uint32],
@@ -244,6 +245,11 @@ def moe_kernels_per_forward(h, S) -> int:
 def moe_selftest_wait_timeout(limit_us: int, stream=None) -> int:
     """Returns the raw status (MOE_ERR_TIMEOUT when the bounded wait works)."""
     return int(lib.moe_selftest_wait_timeout(limit_us, _stream(stream)))
+
+
+def moe_selftest_wait_together(posted: bool, aborted: bool, limit_us: int, stream=None) -> int:
+    """Returns the raw status (MOE_OK, MOE_ERR_TIMEOUT; MOE_ERR_STATE if threads disagreed)."""
+    return int(lib.moe_selftest_wait_together(int(posted), int(aborted), limit_us, _stream(stream)))
 
 
 def moe_assign_slots_noalloc(S, E, k, C, eidx, slot, cnt, stream=None) -> None:

@@ -87,6 +87,37 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_
   return false;
 }
 
+// ---------------------------------------------------------------- waits of several threads
+// The N threads of named barrier ID meet, and all get whether every one (any one) of them brings
+// true: the answer to a wait that some may end and others give up, before anything else that
+// all of them have to reach.
+template <int ID, int N>
+__device__ __forceinline__ bool all_meet(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)mine), "n"(ID), "n"(N)
+      : "memory");
+  return r != 0;
+}
+template <int ID, int N>
+__device__ __forceinline__ bool any_meets(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)mine), "n"(ID), "n"(N)
+      : "memory");
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
                                             int c1) {

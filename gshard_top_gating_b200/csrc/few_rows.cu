@@ -148,9 +148,6 @@ __device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned v) {
   return old;
 }
 
-// The four joining warps meet.
-__device__ __forceinline__ void join_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
 // Finished values of one row: feature f (and f + 128) of a tile.  `live` false: zeros.
 template <int KIND, int ACC, int FN>
 __device__ __forceinline__ void put(const FewArgs& a, int64_t row, int f, const float (&v)[ACC], bool live) {
@@ -199,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* misc = gbase + STAGES * F::STAGE + F::kBars;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  volatile unsigned* arrived = reinterpret_cast<volatile unsigned*>(misc + 8);
   volatile int* ring = reinterpret_cast<volatile int*>(misc + 16);
   Cuts* cuts = reinterpret_cast<Cuts*>(misc + 32);
   volatile int4* joins = reinterpret_cast<volatile int4*>(misc + 64);    // Steps of written parts
@@ -655,8 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a part comes when its depth has been read: a whole share may lie before the first one
       bool got = false;
       for (int tries = 0; !got && tries < 8 && !*abort_flag; ++tries) got = mbar_poll(jfull_bar(slot), (jn / kJoin) & 1, a.limit_ns);
-      if (!got) {
-        if (!*abort_flag && lane == 0) atomicOr(a.err, DEVERR_TIMEOUT);
+      // The four warps go on together or not at all: one that has seen its part wait there, beside
+      // one that has seen the CTA give up and left, would wait for good.
+      if (!all_meet<1, 128>(got)) {
+        if (!got && !*abort_flag) atomicOr(a.err, DEVERR_TIMEOUT);
+        *abort_flag = 1;
         break;
       }
       const Step st{joins[slot].x, joins[slot].y, joins[slot].z, joins[slot].w};
@@ -677,15 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = 2 * i0 + 1;                  // the tile's first CTA, then slot 0 of the next ones
         counter = i0;
       }
+      bool last = false;
       if (lane128 == 0) {
-        const unsigned before = atom_add_acq_rel(a.count + counter, 1u);
-        if (before == (unsigned)parts - 1u) a.count[counter] = 0u;
-        *arrived = before;
+        last = atom_add_acq_rel(a.count + counter, 1u) == (unsigned)parts - 1u;
+        if (last) a.count[counter] = 0u;
       }
-      join_sync();
-      const bool finish = *arrived == (unsigned)parts - 1u;
-      join_sync();                           // all have read it
-      if (!finish) continue;
+      if (!any_meets<1, 128>(last)) continue;
       const Tile t = tile_at(st.t, pre, rtiles, a.E);
       const int row0 = t.rt * NT, nvalid = min(NT, nrows[t.e] - row0);
       const int f = t.nt * F::FEATURES + lane128;

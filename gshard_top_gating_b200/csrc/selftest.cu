@@ -1,9 +1,12 @@
-// selftest.cu -- a kernel whose bounded mbarrier wait is made to run out.
+// selftest.cu -- kernels whose bounded mbarrier waits are made to run out, or their block to
+// give up while they wait.
 //
 // It initialises an mbarrier that nothing will ever arrive on and waits for it
 // with the same bounded-wait helper the tensor-core kernels use.  The wait gives
 // up after limit_ns, sets DEVERR_TIMEOUT in the error word and returns, so the
-// host sees a timeout status and the context stays usable.
+// host sees a timeout status and the context stays usable.  The second kernel's 128 threads
+// wait together, as those that join parts of a tile do (few_rows.cu): they begin some tens of
+// microseconds apart, while another thread says that the block gives up, arrives, or both.
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,7 +28,41 @@ __global__ void wait_selftest_kernel(unsigned* flag, unsigned* err, uint64_t lim
   }
 }
 
+constexpr int kTogether = 128;
+
+// answers[t]: 1 thread t went on, 2 it stopped
+__global__ void together_selftest_kernel(int posted, int aborted, unsigned* answers, unsigned* err, uint64_t limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ volatile int abort_flag;
+  const uint32_t b = smem_u32(&bar);
+  const int t = threadIdx.x;
+  if (t == 0) {
+    mbar_init(b, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (t < kTogether) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < (uint64_t)(t / 32) * 20000u) {}
+    answers[t] = all_meet<1, kTogether>(!abort_flag && mbar_wait(b, 0, err, limit_ns)) ? 1u : 2u;
+  } else if (t == kTogether) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 30000u) {}
+    if (aborted) abort_flag = 1;
+    if (posted) mbar_arrive(b);
+  }
+}
+
 }  // namespace
+
+int selftest_together_threads() { return kTogether; }
+
+cudaError_t launch_together_selftest(bool posted, bool aborted, unsigned* answers, unsigned* err, uint64_t limit_ns,
+                                     cudaStream_t st) {
+  together_selftest_kernel<<<1, kTogether + 32, 0, st>>>(posted, aborted, answers, err, limit_ns);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st) {
   wait_selftest_kernel<<<1, 32, 0, st>>>(flag, err, limit_ns);

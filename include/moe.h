@@ -274,6 +274,15 @@ MOE_API int32_t moe_kernels_per_forward(moe_handle h, int64_t S);
 MOE_API moe_status moe_selftest_wait_timeout(int32_t limit_us, void* stream);
 
 /*
+ * moe_selftest_wait_together -- launch a kernel whose threads wait together for a barrier that
+ * is arrived on (`posted`) or not, while their block gives up (`aborted`) or does not, and
+ * return what they did: MOE_OK when they went on, MOE_ERR_TIMEOUT when they stopped, and
+ * MOE_ERR_STATE when some went on and others stopped, which must not happen.  Leaves the
+ * context usable.  Synchronises `stream`.
+ */
+MOE_API moe_status moe_selftest_wait_together(int32_t posted, int32_t aborted, int32_t limit_us, void* stream);
+
+/*
  * moe_assign_slots_noalloc -- the capacity slot assignment, with no device allocation.
  * (The pages have no counterpart: this is an interface for callers of this library.)
  *
