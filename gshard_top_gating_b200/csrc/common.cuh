@@ -88,6 +88,17 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_
 }
 
 // ---------------------------------------------------------------- waits of several threads
+// mbar_wait by a whole warp that goes on with instructions of all its lanes (tcgen05.ld, shuffles,
+// __syncwarp): lanes may see the block give up, or the limit pass, at different times, so they
+// vote.  Where one gave up all stop, and the block is told.
+__device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint32_t bar, uint32_t parity, unsigned* err,
+                                          uint64_t limit_ns) {
+  const bool ok = mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, err, limit_ns));
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *abort_flag = 1;
+  return false;
+}
+
 // The N threads of named barrier ID meet, and all get whether every one (any one) of them brings
 // true: the answer to a wait that some may end and others give up, before anything else that
 // all of them have to reach.

@@ -484,8 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // passes a written part (or, with len 0, the end) on to the joining warps
     auto pass_on = [&](const Step& st) {
       const int slot = jn % kJoin;
-      if (*abort_flag || !mbar_wait(jempty_bar(slot), ((jn / kJoin) & 1) ^ 1, a.err, a.limit_ns)) {
-        *abort_flag = 1;
+      if (!warp_wait(abort_flag, jempty_bar(slot), ((jn / kJoin) & 1) ^ 1, a.err, a.limit_ns)) {
         ok = false;
         return;
       }
@@ -525,8 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           xv = i < st.len && lane < nvalid ? __ldg(xs + (int64_t)lane * KB + kb) : 0.f;
         };
         auto drain = [&](int i, float& xv, float (&wv)[ACC]) {
-          if (*abort_flag || !mbar_wait(tfull_bar(buf), bph, a.err, a.limit_ns)) {
-            *abort_flag = 1;
+          if (!warp_wait(abort_flag, tfull_bar(buf), bph, a.err, a.limit_ns)) {
             ok = false;
             return;
           }
@@ -582,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       } else {
-        if (*abort_flag || !mbar_wait(tfull_bar(buf), bph, a.err, a.limit_ns)) {
-          *abort_flag = 1;
+        if (!warp_wait(abort_flag, tfull_bar(buf), bph, a.err, a.limit_ns)) {
           ok = false;
           return;
         }
@@ -631,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (npieces > 0)
       for (int r = 0; ok; ++r) {
         const int slot = r % kRing;
-        if (*abort_flag || !mbar_wait(pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
-          *abort_flag = 1;
+        if (!warp_wait(abort_flag, pfull_bar(slot), (r / kRing) & 1, a.err, a.limit_ns)) {
+          ok = false;
           break;
         }
         const int id = ring[slot];

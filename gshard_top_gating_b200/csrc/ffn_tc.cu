@@ -450,10 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < BN / 32; ++w) bw[w] = __ldg(brow + w * bstride);
       }
-      if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, err, limit_ns)) {
-        *abort_flag = 1;
-        break;
-      }
+      if (!warp_wait(abort_flag, tfull_bar(acc), aph, err, limit_ns)) break;
       tc_fence_after();
       if (row0 < row_limit)           // a store box starts inside the tensor (TMA clips its tail)
         store_rows<BN, EPI>(&tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN, stage, row0,
@@ -650,10 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc = i & 1;
         const uint32_t aph = (i >> 1) & 1;
         ++i;
-        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, err, limit_ns)) {
-          *abort_flag = 1;
-          break;
-        }
+        if (!warp_wait(abort_flag, tfull_bar(acc), aph, err, limit_ns)) break;
         tc_fence_after();
       }
       if (prow < P && (!zero || store_zero))
@@ -896,10 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < BN / 32; ++w) bw[w] = __ldg(brow + w * bstride);
       }
-      if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, err, limit_ns)) {
-        *abort_flag = 1;
-        break;
-      }
+      if (!warp_wait(abort_flag, tfull_bar(acc), aph, err, limit_ns)) break;
       tc_fence_after();
       store_rows<BN, EPI>(&tmD, tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN, stage, row0,
                           nt * BN, lane, mrow, false, brow, bw, bstride, &sy,
@@ -1085,10 +1076,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         acc = i & 1;
         const uint32_t aph = (i >> 1) & 1;
         ++i;
-        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, err, limit_ns)) {
-          *abort_flag = 1;
-          break;
-        }
+        if (!warp_wait(abort_flag, tfull_bar(acc), aph, err, limit_ns)) break;
         tc_fence_after();
       }
       if (prow < P && (!zero || store_zero))

@@ -254,10 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // adds block kb; its scales were loaded four blocks ago, those of block kb + 4 are now
       auto drain = [&](int kb, float& x, float& w) -> bool {
-        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
-          *abort_flag = 1;
-          return false;
-        }
+        if (!warp_wait(abort_flag, tfull_bar(acc), aph, a.err, a.limit_ns)) return false;
         tc_fence_after();
         const float f = x * w;
         const uint64_t sc = pack_f32x2(f, f);

@@ -475,8 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
           tma_prefetch_l2_2d(&tmD2, a.N + col0 + b * 32, (int)row0);
         }
       }
-      if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
-        *abort_flag = 1;
+      if (!warp_wait(abort_flag, tfull_bar(acc), aph, a.err, a.limit_ns)) {
         if (MODE == kDh && nvalid > 0 && col0 < a.N) mbar_wait(gu_bar(warp - 2, 0), gph & 1u, a.err, a.limit_ns);
         break;
       }
@@ -752,10 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
         acc = i & 1;
         const uint32_t aph = (i >> 1) & 1;
         ++i;
-        if (*abort_flag || !mbar_wait(tfull_bar(acc), aph, a.err, a.limit_ns)) {
-          *abort_flag = 1;
-          break;
-        }
+        if (!warp_wait(abort_flag, tfull_bar(acc), aph, a.err, a.limit_ns)) break;
         tc_fence_after();
       }
       if (prow < d.P && (!zero || a.store_zero))

@@ -361,9 +361,11 @@ cudaError_t fp8_quantize_glu(int E, int64_t C, int K, int fn, const int32_t* n, 
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st);
 // selftest.cu
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st);
-// answers: one word for each of selftest_together_threads()
-int selftest_together_threads();
+// answers: kSelftestAnswers words, device; on the host, whether threads that wait together agree in
+// them, and whether any stopped
+constexpr int kSelftestAnswers = 512;
 cudaError_t launch_together_selftest(bool posted, bool aborted, unsigned* answers, unsigned* err, uint64_t limit_ns,
                                      cudaStream_t st);
+bool selftest_together_agrees(const unsigned* answers, bool* stopped);
 
 }  // namespace moe

@@ -1083,22 +1083,20 @@ moe_status moe_selftest_wait_timeout(int32_t limit_us, void* stream) {
 
 moe_status moe_selftest_wait_together(int32_t posted, int32_t aborted, int32_t limit_us, void* stream) {
   if (limit_us < 0 || limit_us > 10000000) return MOE_ERR_INVALID_ARG;
-  constexpr int kMost = 512;
-  const int n = selftest_together_threads();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned* buf = nullptr;
-  MOE_TRY(cudaMalloc(&buf, (kMost + 1) * sizeof(unsigned)));
-  unsigned host[kMost] = {};
-  cudaError_t ce = cudaMemsetAsync(buf, 0, (kMost + 1) * sizeof(unsigned), st);
+  unsigned host[kSelftestAnswers] = {};
+  MOE_TRY(cudaMalloc(&buf, sizeof(host) + sizeof(unsigned)));
+  cudaError_t ce = cudaMemsetAsync(buf, 0, sizeof(host) + sizeof(unsigned), st);
   if (ce == cudaSuccess)
-    ce = launch_together_selftest(posted != 0, aborted != 0, buf, buf + kMost, (uint64_t)limit_us * 1000ull, st);
+    ce = launch_together_selftest(posted != 0, aborted != 0, buf, buf + kSelftestAnswers, (uint64_t)limit_us * 1000ull, st);
   if (ce == cudaSuccess) ce = cudaMemcpyAsync(host, buf, sizeof(host), cudaMemcpyDeviceToHost, st);
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
   cudaFree(buf);
   if (ce != cudaSuccess) return from_cuda(ce);
-  for (int i = 0; i < n; ++i)
-    if ((host[i] != 1u && host[i] != 2u) || host[i] != host[0]) return MOE_ERR_STATE;
-  return host[0] == 1u ? MOE_OK : MOE_ERR_TIMEOUT;
+  bool stopped = false;
+  if (!selftest_together_agrees(host, &stopped)) return MOE_ERR_STATE;
+  return stopped ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 
 }  // extern "C"

@@ -262,8 +262,7 @@ __global__ void __launch_bounds__(NW * 32, (NW == 8) ? 2 : 1)
     const int nseg = (KB + kSegBlocks - 1) / kSegBlocks;
     bool ok = true;
     for (int seg = 0; seg < nseg; ++seg) {
-      if (*abort_flag || !mbar_wait(tfull_bar, seg & 1, R.err, limit_ns)) {
-        *abort_flag = 1;
+      if (!warp_wait(abort_flag, tfull_bar, seg & 1, R.err, limit_ns)) {
         ok = false;
         break;
       }

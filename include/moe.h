@@ -276,9 +276,9 @@ MOE_API moe_status moe_selftest_wait_timeout(int32_t limit_us, void* stream);
 /*
  * moe_selftest_wait_together -- launch a kernel whose threads wait together for a barrier that
  * is arrived on (`posted`) or not, while their block gives up (`aborted`) or does not, and
- * return what they did: MOE_OK when they went on, MOE_ERR_TIMEOUT when they stopped, and
- * MOE_ERR_STATE when some went on and others stopped, which must not happen.  Leaves the
- * context usable.  Synchronises `stream`.
+ * return what they did: MOE_OK when they went on, MOE_ERR_TIMEOUT when any stopped, and
+ * MOE_ERR_STATE when some went on and others of the same warp, or of the warps that wait
+ * together, stopped, which must not happen.  Leaves the context usable.  Synchronises `stream`.
  */
 MOE_API moe_status moe_selftest_wait_together(int32_t posted, int32_t aborted, int32_t limit_us, void* stream);
 
