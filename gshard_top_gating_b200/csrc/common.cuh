@@ -99,6 +99,16 @@ __device__ __forceinline__ bool warp_wait(volatile int* abort_flag, uint32_t bar
   return false;
 }
 
+// Before the barrier at the end of a kernel whose block may have given up: TMA copies in flight, which
+// nobody waits for any more, still write to the block's shared memory and signal its barriers
+// or, in a pair, the first block's.  They land within microseconds; the block stays 1 ms.  Who
+// sets the flag passes here after it, and who copies reads it before each copy.
+__device__ __forceinline__ void let_copies_land(volatile int* abort_flag) {
+  if (*abort_flag == 0) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
+}
+
 // The N threads of named barrier ID meet, and all get whether every one (any one) of them brings
 // true: the answer to a wait that some may end and others give up, before anything else that
 // all of them have to reach.

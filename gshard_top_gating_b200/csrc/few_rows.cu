@@ -731,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

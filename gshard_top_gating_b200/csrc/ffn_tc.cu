@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -904,6 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncwarp();
   cluster_sync_all();          // no CTA leaves while its pair may still use its smem or TMEM
   if (warp == 1) {
@@ -1093,6 +1096,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncwarp();
   cluster_sync_all();          // no CTA leaves while its pair may still use its smem or TMEM
   if (warp == 1) {

@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(NW * 32, (NW == 8) ? 2 : 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -923,6 +924,7 @@ __global__ void __launch_bounds__(512, 1)
   }
 
   tc_fence_before();
+  let_copies_land(abort_flag);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

@@ -9,6 +9,9 @@ different barriers, which never fill; where all meet and go by what all have see
 """
 from __future__ import annotations
 
+import os
+import re
+
 import pytest
 
 WARPS = 4
@@ -60,3 +63,20 @@ def test_threads_that_wait_together_go_on_or_stop_together(posted, aborted):
     allowed = {L.MOE_OK} if posted and not aborted else {L.MOE_ERR_TIMEOUT} if not posted else {L.MOE_OK, L.MOE_ERR_TIMEOUT}
     for _ in range(20):
         assert L.moe_selftest_wait_together(posted, aborted, 2000) in allowed
+
+
+def test_a_block_that_gave_up_lets_its_copies_land():
+    """Each kernel with an abort flag goes through let_copies_land once, right before the barrier at
+    its end and the release of its TMEM."""
+    here = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gshard_top_gating_b200", "csrc")
+    end = re.compile(r"let_copies_land\(abort_flag\);\n(?:  __syncwarp\(\);\n)?  (?:__syncthreads|cluster_sync_all)\(\);[^\n]*\n"
+                     r"  if \(warp == 1\) \{\n    tc_fence_after\(\);\n    tmem_dealloc")
+    kernels = 0
+    for name in sorted(os.listdir(here)):
+        if name.endswith(".cu"):
+            with open(os.path.join(here, name)) as f:
+                text = f.read()
+            flags = text.count("volatile int* abort_flag = ")
+            assert flags == len(end.findall(text)) == text.count("let_copies_land("), name
+            kernels += flags
+    assert kernels >= 10
