@@ -35,11 +35,11 @@ __device__ __forceinline__ float glu_f(float g) {
     normal_fast(g, c, d);
     return g * c;
   }
-  return fmaxf(g, 0.f);
+  return g <= 0.f ? 0.f : g;      // a NaN stays one
 }
 
 // f(g) and f'(g): silu s(1 + g(1 - s)), s = 1/(1 + e^-g); gelu F(g) + g e^(-g^2/2)/sqrt(2 pi)
-// with F the normal distribution; relu 1 for g > 0.
+// with F the normal distribution; relu 1 for g > 0.  Where g is NaN both are, for every f.
 template <int FN, bool FAST>
 __device__ __forceinline__ void glu_f_df(float g, float& f, float& df) {
   if (FN == kGluSilu) {
@@ -57,8 +57,8 @@ __device__ __forceinline__ void glu_f_df(float g, float& f, float& df) {
     f = g * c;
     df = fmaf(g, d, c);
   } else {
-    f = fmaxf(g, 0.f);
-    df = g > 0.f ? 1.f : 0.f;
+    f = g <= 0.f ? 0.f : g;
+    df = g > 0.f ? 1.f : f;       // 0, or NaN
   }
 }
 

@@ -101,7 +101,7 @@ MOE_API moe_status moe_create(moe_handle* out, int64_t S_max, int64_t M, int64_t
 typedef enum {
   MOE_GLU_SILU = 0,      /* f(g) = g / (1 + e^-g) */
   MOE_GLU_GELU = 1,      /* f(g) = g (1 + erf(g / sqrt 2)) / 2 */
-  MOE_GLU_RELU = 2       /* f(g) = max(g, 0), f'(0) = 0 */
+  MOE_GLU_RELU = 2       /* f(g) = max(g, 0), NaN for NaN; f'(0) = 0 */
 } moe_glu_fn;
 
 /*
