@@ -65,17 +65,21 @@ __device__ __forceinline__ void glu_f_df(float g, float& f, float& df) {
 // g and u as a bf16 forward keeps them for its backward, in 16 bits, 32 columns of a row alike:
 // fp16 where all their magnitudes are in [2^-17, 65504), which is never less exact than bf16 and
 // from 2^-14 on eight times more so, else bf16.  The lowest bit of the first of the 32 says which
-// (1: fp16); that one is off by at most 1.5 2^-10 in fp16, 2^-7 in bf16.  dx and dW13 are then
+// (1: fp16).  That one becomes the nearest code with this lowest bit, either way, so it is off by
+// at most a step where the others are by half of one: 2^-10 of itself in fp16 (2^-24 in all
+// below 2^-14, where fp16 is subnormal), 2^-7 in bf16.  dx and dW13 are then
 // off by 2.4e-3 of their norm, the roundings of dg, du and the results; with g and u in bf16
 // alone by 3.0e-3, for 1 to 3% less time (15 experts of 1365 rows, M = 256, H = 3008: 325 us
 // against 348, as the epilogues of `up` and `dh` bound small M).
 __device__ __forceinline__ bool gu_fine(float least, float most) { return least >= 0x1p-17f && most < 65504.f; }
 __device__ __forceinline__ bool gu_is_fine(uint32_t first) { return first & 1u; }
-// The first of 32 in bf16, rounded to an even code.
+// The first of 32 in bf16, rounded to the nearest even code.
 __device__ __forceinline__ uint32_t gu_first_wide(float v) {
   const uint32_t x = __float_as_uint(v);
   return (min((x & 0x7fffffffu) + 0x10000u, 0x7fffffffu) >> 16 & 0x7ffeu) | (x >> 16 & 0x8000u);
 }
+// In fp16, to an odd code: towards zero, which leaves 2k or 2k + 1, then 2k + 1.
+__device__ __forceinline__ uint32_t gu_first_fine(float v) { return __half_as_ushort(__float2half_rz(v)) | 1u; }
 __device__ __forceinline__ void pack_gu(const uint32_t (&v)[32], bool live, uint32_t (&pk)[16]) {
   float least = fabsf(__uint_as_float(v[0])), most = least;
 #pragma unroll
@@ -90,14 +94,17 @@ __device__ __forceinline__ void pack_gu(const uint32_t (&v)[32], bool live, uint
     const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
     pk[j] = !live ? 0u : fine ? pack_f16x2(a, b) : pack_bf16x2(a, b);
   }
-  if (live) pk[0] = fine ? pk[0] | 1u : (pk[0] & 0xffff0000u) | gu_first_wide(__uint_as_float(v[0]));
+  if (live) {
+    const float first = __uint_as_float(v[0]);
+    pk[0] = (pk[0] & 0xffff0000u) | (fine ? gu_first_fine(first) : gu_first_wide(first));
+  }
 }
 // One of them, where the warp holds the 32 columns (and the row is live for all of it or none).
 __device__ __forceinline__ uint16_t pack_gu_lane(float v, bool live) {
   const float m = fabsf(v);
   const bool fine = __all_sync(0xffffffffu, gu_fine(m, m) || isnan(v));
   uint32_t c = (fine ? pack_f16x2(v, 0.f) : pack_bf16x2(v, 0.f)) & 0xffffu;
-  if ((threadIdx.x & 31) == 0) c = fine ? c | 1u : gu_first_wide(v);
+  if ((threadIdx.x & 31) == 0) c = fine ? gu_first_fine(v) : gu_first_wide(v);
   return live ? (uint16_t)c : 0;
 }
 // Both of a word: FINE, all lanes hold fp16; else each lane as `fine` says.

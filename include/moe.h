@@ -590,8 +590,10 @@ MOE_API const char* moe_backward_stage_name(int32_t stage);
  *
  * with W13 = [Wg | Wu] and f one of moe_glu_fn.  Both projections, f and the product are
  * one kernel, and so are dh, dg and du.  Arithmetic is fp32 throughout (sums over the
- * depth included); with bf16 the stored h, g, u, dg and du are rounded to bf16, as the
- * operands of the products that follow, and so are the results.
+ * depth included); with bf16 the stored h, dg and du are rounded to bf16, as the operands of
+ * the products that follow, and so are the results.  g and u wait for the backward in 16
+ * bits: 32 columns of a row as fp16 where all their magnitudes are in [2^-17, 65504), else
+ * as bf16; the first of the 32 is off by up to a step of its form, the others by half.
  *
  * Rows: x, y, dy and dx are [E, C, M] act, and nrows_dev [E] int32 (device) says how many
  * of its C rows each expert holds, read as min(max(nrows, 0), C).  Rows past that are not
