@@ -2,11 +2,18 @@
 
 Tolerances, from the arithmetic:
 
+gelu far below 0: f(g) = g F(g), F the normal distribution.  Its approximation is off by
+2^-17.9 of itself; the exponential's argument -g^2 / 2 carries two roundings, 2 * 2^-24 * 40.5
+of the result at g = -9, and the hardware exponential 2 + 1.173 * 40.5 units of 2^-23: in all
+below 2^-15.  What is stored of it is rounded to bf16 once, 2^-8.
+
 g and u between the passes: 32 columns of a row as fp16 where they fit it.  The first of the 32
 is the nearest of the odd codes, so within a step: 2^-24 below 2^-14.  A code of at most 8
 bits is exact in bf16, so du = dh f(g) of such a g shows it as it was kept.
 """
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -16,6 +23,7 @@ from .test_gpu_glu import experts, make
 pytestmark = pytest.mark.gpu
 
 PATHS = pytest.mark.parametrize("C", [5, 70], ids=["few rows", "tiles"])
+U = torch.finfo(torch.bfloat16).eps / 2
 
 
 @PATHS
@@ -72,6 +80,31 @@ def in_capacity(t, C):
     out = torch.full((t.shape[0], C, t.shape[2]), float("nan"), dtype=t.dtype, device="cuda")
     out[:, :1] = t
     return out
+
+
+@PATHS
+def test_gelu_far_below_zero(C):
+    """All gates between -5 and -9: h and the gradients through it, relative to their value."""
+    gate = torch.zeros(3, 2, 64, device="cuda")
+    gate[:, 0] = -torch.linspace(5, 9, 192, device="cuda").view(3, 64)
+    x, W13, W2, n = unit_experts(3, 64, gate)
+    x = in_capacity(x, C)
+    ex = experts(C, W13, W2, "gelu")
+    y = ex(x, n)[:, 0].double()
+    g = ex.backward(x, n, torch.ones_like(x))
+    z = W13[:, 0, :64].double()
+    phi = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    cdf = 0.5 * torch.erfc(-z * 0.5**0.5)               # (1 + erf would lose its digits here)
+    f, df = z * cdf, cdf + z * phi
+    bar = U + 2.0**-15
+    assert bool(((y - f).abs() <= bar * f.abs()).all()), float(((y - f) / f).abs().max())
+    dW2 = g["dW2"].double()[:, :, 0]                    # h^T dy, dy = 1
+    assert bool(((dW2 - f).abs() <= bar * f.abs()).all())
+    # g as kept between the passes is exact but for the first of 32
+    keep = torch.arange(64, device="cuda") % 32 != 0
+    for got, want in ((g["dW13"][:, 0, 64:], f), (g["dW13"][:, 0, :64], df)):
+        d = ((got.double() - want).abs() / want.abs())[:, keep]
+        assert bool((d <= U + 2.0**-14).all()), float(d.max())
 
 
 @PATHS
