@@ -10,6 +10,12 @@ below 2^-15.  What is stored of it is rounded to bf16 once, 2^-8.
 g and u between the passes: 32 columns of a row as fp16 where they fit it.  The first of the 32
 is the nearest of the odd codes, so within a step: 2^-24 below 2^-14.  A code of at most 8
 bits is exact in bf16, so du = dh f(g) of such a g shows it as it was kept.
+
+Norms in bf16, inputs normal: one rounding of such values is off by 1.65e-3 of their norm.  Two
+independent ones (y: h and y; dW2: h and dW2) by 2.34e-3; dx and dW13 (dg and du, the result)
+likewise, as g and u in fp16 add 0.2e-3 each; with g and u in bf16 it would be three, 2.9e-3.
+The same steps in 64 bits with these roundings give 2.16e-3 to 2.41e-3 (3.0e-3 with g and u in
+bf16) over shapes of 5 to 300 rows: bars of 2.6e-3 and 2.7e-3.
 """
 from __future__ import annotations
 
@@ -18,7 +24,7 @@ import math
 import pytest
 import torch
 
-from .test_gpu_glu import experts, make
+from .test_gpu_glu import act, experts, make
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +130,25 @@ def test_first_of_32_small_gates_is_kept_within_a_step(C, rest):
     du = ex.backward(x, n, torch.ones_like(x))["dW13"][:, 0, 64].double()
     want = W13[:, 0, 0].double() + W13[:, 1, 0].double()
     assert bool(((du - want).abs() <= step * (1 + 2.0**-10)).all()), float(((du - want) / step).abs().max())
+
+
+@pytest.mark.parametrize("fn", ["silu", "gelu"])
+@pytest.mark.parametrize("case", [(16, 8, 256, 512, "few rows"), (3, 70, 256, 512, "tiles"), (2, 300, 128, 320, "tiles of 300")],
+                         ids=lambda c: c[4])
+def test_norm_of_the_error_is_that_of_its_roundings(case, fn):
+    E, C, M, H, _ = case
+    x, dy, W13, W2, n = make(E, C, M, H, torch.bfloat16, [C] * E, seed=11)
+    ex = experts(C, W13, W2, fn)
+    y = ex(x, n)
+    g = ex.backward(x, n, dy)
+    X, D, Wg, Wu, W = (t.double() for t in (x, dy, W13[:, :, :H], W13[:, :, H:], W2))
+    gate, up = X @ Wg, X @ Wu
+    f, df = act(fn, gate)
+    h, dh = f * up, D @ W.transpose(1, 2)
+    dg, du = dh * up * df, dh * f
+    want = {"y": h @ W, "dW2": h.transpose(1, 2) @ D, "dx": dg @ Wg.transpose(1, 2) + du @ Wu.transpose(1, 2),
+            "dW13": X.transpose(1, 2) @ torch.cat([dg, du], 2)}
+    for name, bar in (("y", 2.6e-3), ("dW2", 2.6e-3), ("dx", 2.7e-3), ("dW13", 2.7e-3)):
+        got = (y if name == "y" else g[name]).double()
+        off = float((got - want[name]).norm() / want[name].norm())
+        assert off <= bar, (name, off)
