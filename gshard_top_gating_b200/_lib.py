@@ -132,7 +132,7 @@ def _check(fn: str, status: int) -> None:
 def _ptr(t) -> int | None:
     if isinstance(t, torch.Tensor):
         return t.data_ptr()
-    return t
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> int | None:
