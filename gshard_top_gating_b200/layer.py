@@ -50,6 +50,7 @@ class MoeLayer:
         self.cf = capacity_factor
         self.act = act
         self._keep = (Wg, gate_bias, W1, W2)
+        self._device = Wg.get_device()
         self.W1_cols = H if activation is None else 2 * H
         if fp8:
             self._keep += (W1s, W2s)
@@ -66,10 +67,24 @@ class MoeLayer:
             raise ValueError("x must be a contiguous [S, M] tensor of the activation dtype")
         S = x.shape[0]
         y = out if out is not None else torch.empty_like(x)
+        if out is not None or not x.is_cuda:
+            self._check_buffers(("x", x, x.numel(), self.act), ("out", y, x.numel(), self.act))
         L.moe_forward(self.h, S, x, y, stream)
         return y
 
+    def _check_buffers(self, *buffers) -> None:
+        """Refuse memory that the kernels would read or write past its end, or could not reach."""
+        for name, t, n, dtype in buffers:
+            if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+                raise ValueError(f"{name} must be contiguous and hold {n} values of {dtype}, not {tuple(t.shape)} of {t.dtype}")
+            if not (t.get_device() == self._device if t.is_cuda else t.is_pinned()):
+                raise ValueError(f"{name} must be on the layer's GPU, not on {t.device}")
+
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, stream=None) -> None:
+        n = x_host.shape[0] * self.M
+        for name, t in (("x_host", x_host), ("y_host", y_host)):
+            if t.dtype != self.act or not t.is_contiguous() or t.numel() < n:
+                raise ValueError(f"{name} must be contiguous and hold {n} values of {self.act}, not {tuple(t.shape)} of {t.dtype}")
         L.moe_forward_host(self.h, x_host.shape[0], x_host, y_host, stream)
 
     def aux_loss(self, stream=None):
@@ -111,9 +126,13 @@ class MoeLayer:
             torch.empty(self.E, self.M, self.W1_cols, dtype=self.act, device=dev)
         dW2 = out.get("dW2") if out.get("dW2") is not None else \
             torch.empty(self.E, self.H, self.M, dtype=self.act, device=dev)
-        for t in (dx, dWg, dW1, dW2) + ((dbias,) if dbias is not None else ()):
-            if not (t.is_cuda and t.is_contiguous()):
+        n, M, E, f32 = x.numel(), self.M, self.E, torch.float32
+        grads = [("dx", dx, n, self.act), ("dWg", dWg, M * E, f32), ("dW1", dW1, E * M * self.W1_cols, self.act),
+                 ("dW2", dW2, E * self.H * M, self.act)] + ([("dbias", dbias, E, f32)] if dbias is not None else [])
+        for _, t, _, _ in grads:
+            if not t.is_cuda:
                 raise ValueError("gradient buffers must be contiguous CUDA tensors")
+        self._check_buffers(("x", x, n, self.act), ("dy", dy, n, self.act), *grads)
         L.moe_set_backward_flags(self.h, L.MOE_BWD_SKIP_EMPTY_EXPERTS if skip_empty_experts else 0)
         L.moe_backward(self.h, S, x, dy, a_aux, a_z, dx, dWg, dbias, dW1, dW2, stream)
         return {"dx": dx, "dWg": dWg, "dbias": dbias, "dW1": dW1, "dW2": dW2}
