@@ -400,7 +400,7 @@ cudaError_t fp8_pair(const Fp8Args& a) {
   p.splits = fp8_shares(a);
   if (p.splits == 1) return launch<64, false>(tmA, tmD, p, a);
   const cudaError_t e = launch<64, true>(tmA, tmD, p, a);
-  return e != cudaSuccess ? e : split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.st);
+  return e != cudaSuccess ? e : split_join(a.part, a.y, true, a.n, a.E, a.rows, a.C, a.N, p.splits, a.num_sms, a.st);
 }
 
 }  // namespace moe

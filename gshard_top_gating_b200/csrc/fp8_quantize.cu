@@ -196,7 +196,12 @@ cudaError_t launch_rows(uint32_t nblocks, uint32_t KB, int K, const void* x, voi
   // many blocks: several in flight per lane group (65536 x 7168 bf16: 267 us with one, 244 with
   // two, 229 with four, 224 with eight; copying the same bytes 218); few: one each, on more SMs
   constexpr int MANY = BF16 ? 8 : 4;
-  const bool many = nblocks >= 148u * 128u * MANY;
+  int dev = 0, sms = 148;
+  if (nblocks >= 128u * MANY) {          // (few rows: not worth the question)
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  }
+  const bool many = nblocks >= (uint32_t)sms * 128u * MANY;
   const uint32_t per = 16u * (many ? MANY : 1);
   const dim3 grid((nblocks + per - 1) / per);
   auto kern = many ? quantize_rows_kernel<BF16, EVEN, MANY> : quantize_rows_kernel<BF16, EVEN, 1>;
@@ -215,10 +220,11 @@ cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* 
 namespace {
 
 template <int FN>
-cudaError_t launch_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s, cudaStream_t st) {
+cudaError_t launch_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s, int num_sms,
+                        cudaStream_t st) {
   const uint32_t KB = (uint32_t)((K + 127) / 128);
   // about eight blocks of threads per SM over all experts, and no more than an expert can use
-  int64_t per = (C * KB + 15) / 16, want = (148 * 8 + E - 1) / E;
+  int64_t per = (C * KB + 15) / 16, want = (num_sms * 8 + E - 1) / E;
   if (want > per) want = per;
   return launch_pdl(quantize_held_kernel<FN>, dim3((unsigned)want, E), dim3(256), 0, st, x, static_cast<uint2*>(q), s, n, C,
                     KB, K);
@@ -226,16 +232,16 @@ cudaError_t launch_held(int E, int64_t C, int K, const int32_t* n, const void* x
 
 }  // namespace
 
-cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s,
+cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s, int num_sms,
                               cudaStream_t st) {
-  return launch_held<-1>(E, C, K, n, x, q, s, st);
+  return launch_held<-1>(E, C, K, n, x, q, s, num_sms, st);
 }
 
 cudaError_t fp8_quantize_glu(int E, int64_t C, int K, int fn, const int32_t* n, const void* gu, void* q, float* s,
-                             cudaStream_t st) {
-  if (fn == kGluSilu) return launch_held<kGluSilu>(E, C, K, n, gu, q, s, st);
-  if (fn == kGluGelu) return launch_held<kGluGelu>(E, C, K, n, gu, q, s, st);
-  return launch_held<kGluRelu>(E, C, K, n, gu, q, s, st);
+                             int num_sms, cudaStream_t st) {
+  if (fn == kGluSilu) return launch_held<kGluSilu>(E, C, K, n, gu, q, s, num_sms, st);
+  if (fn == kGluGelu) return launch_held<kGluGelu>(E, C, K, n, gu, q, s, num_sms, st);
+  return launch_held<kGluRelu>(E, C, K, n, gu, q, s, num_sms, st);
 }
 
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st) {

@@ -277,7 +277,7 @@ cudaError_t launch_shares(SimtArgs g, const GluArgs& a, int K, float* out) {
   g.s_z = a.E * g.d_z;
   const cudaError_t e = launch<false, BT, kSPlain, kGluSilu>(g, a.rows, g.cols, a.E, a.num_sms, a.st);
   if (e != cudaSuccess) return e;
-  return split_join(a.part, out, false, a.n, a.E, a.rows, a.C, g.cols, s, a.st);
+  return split_join(a.part, out, false, a.n, a.E, a.rows, a.C, g.cols, s, a.num_sms, a.st);
 }
 
 template <bool AT, bool BT, int EPI>

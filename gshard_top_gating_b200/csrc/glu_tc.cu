@@ -822,7 +822,7 @@ cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB, const C
   p.part = a.part;
   const cudaError_t e = launch_pair<MODE, kGluSilu>(tmA, tmB, tmD, tmD, p, a);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return split_join(a.part, out, true, a.n, a.E, a.rows, a.C, p.N, p.splits, a.st);
+  return split_join(a.part, out, true, a.n, a.E, a.rows, a.C, p.N, p.splits, a.num_sms, a.st);
 }
 
 uint64_t rows(int E, int64_t per) { return (uint64_t)E * (uint64_t)per; }

@@ -342,7 +342,7 @@ cudaError_t fp8_pair(const Fp8Args& a);         // tiles of 256 x 256, 128 or 64
 int split_count(int E, int64_t rows, int N, int TN, int KB, double block_us, int num_sms);
 size_t split_workspace(int E, int N, int num_sms);
 cudaError_t split_join(const float* part, void* y, bool bf16, const int32_t* n, int E, int64_t rows, int64_t C, int N,
-                       int splits, cudaStream_t st);
+                       int splits, int num_sms, cudaStream_t st);
 // few_rows.cu: the same products (gated experts' up and down in bf16, the 8-bit one) for few
 // rows.  Workspace: floats of partial sums (returned) and counts, zero before the first
 // launch; every launch leaves the counts zero.
@@ -354,10 +354,10 @@ cudaError_t fp8_few(const Fp8Args& a);
 cudaError_t fp8_quantize_rows(int64_t R, int K, bool bf16, const void* x, void* q, float* s, cudaStream_t st);
 // The rows each expert holds of x [E, C, K] bf16 (n as in Fp8Args); and the same of
 // h = f(g) * u, [g | u] = gu [E, C, 2K] bf16.
-cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s,
+cudaError_t fp8_quantize_held(int E, int64_t C, int K, const int32_t* n, const void* x, void* q, float* s, int num_sms,
                               cudaStream_t st);
 cudaError_t fp8_quantize_glu(int E, int64_t C, int K, int fn, const int32_t* n, const void* gu, void* q, float* s,
-                             cudaStream_t st);
+                             int num_sms, cudaStream_t st);
 cudaError_t fp8_quantize_weights(int E, int K, int N, bool bf16, const void* W, void* q, float* s, cudaStream_t st);
 // selftest.cu
 cudaError_t launch_wait_selftest(unsigned* flag, unsigned* err, uint64_t limit_ns, cudaStream_t st);

@@ -582,10 +582,10 @@ moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStr
     MOE_TRY(launch_dispatch(x, bf16, iS, iM, h->E, h->k, C, h->Cbuf, R, h->xbuf, st));
   MOE_TRY(mark(3));
   if (h->fp8) {
-    MOE_TRY(fp8_quantize_held(h->E, h->Cbuf, iM, R.nexp, h->xbuf, h->xq, h->xs, st));
+    MOE_TRY(fp8_quantize_held(h->E, h->Cbuf, iM, R.nexp, h->xbuf, h->xq, h->xs, h->num_sms, st));
     MOE_TRY(fp8_matmul(fp8_args(h, S, st, h->xq, h->xs, iM, h->W1, h->W1s, 2 * iH, h->gu)));
     MOE_TRY(mark(4));
-    MOE_TRY(fp8_quantize_glu(h->E, h->Cbuf, iH, h->fn, R.nexp, h->gu, h->hq, h->hs, st));
+    MOE_TRY(fp8_quantize_glu(h->E, h->Cbuf, iH, h->fn, R.nexp, h->gu, h->hq, h->hs, h->num_sms, st));
     MOE_TRY(fp8_matmul(fp8_args(h, S, st, h->hq, h->hs, iH, h->W2, h->W2s, iM, h->ybuf)));
   } else if (h->gated) {
     const GluArgs a = glu_args(h, S, st);

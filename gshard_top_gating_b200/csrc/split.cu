@@ -81,8 +81,8 @@ namespace {
 
 template <typename T>
 cudaError_t launch_join(const float* part, T* y, const int32_t* n, int E, int64_t rows, int64_t C, int N, int splits,
-                        cudaStream_t st) {
-  const int64_t work = (rows * (N / 8) + 255) / 256, most = (148 * 8 + E - 1) / E;
+                        int num_sms, cudaStream_t st) {
+  const int64_t work = (rows * (N / 8) + 255) / 256, most = (num_sms * 8 + E - 1) / E;
   return launch_pdl(split_join_kernel<T>, dim3((unsigned)(work < most ? work : most), E), dim3(256), 0, st, part, y, n,
                     (int)rows, C, N, splits);
 }
@@ -90,9 +90,9 @@ cudaError_t launch_join(const float* part, T* y, const int32_t* n, int E, int64_
 }  // namespace
 
 cudaError_t split_join(const float* part, void* y, bool bf16, const int32_t* n, int E, int64_t rows, int64_t C, int N,
-                       int splits, cudaStream_t st) {
-  if (bf16) return launch_join(part, static_cast<__nv_bfloat16*>(y), n, E, rows, C, N, splits, st);
-  return launch_join(part, static_cast<float*>(y), n, E, rows, C, N, splits, st);
+                       int splits, int num_sms, cudaStream_t st) {
+  if (bf16) return launch_join(part, static_cast<__nv_bfloat16*>(y), n, E, rows, C, N, splits, num_sms, st);
+  return launch_join(part, static_cast<float*>(y), n, E, rows, C, N, splits, num_sms, st);
 }
 
 }  // namespace moe
