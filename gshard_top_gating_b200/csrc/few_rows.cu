@@ -3,8 +3,9 @@
 // has to be read, so they stream through every SM, and the rows ride along.
 //
 // The product is transposed: a tile is 128 or 256 columns of the result (features; `up`: 128 of
-// g and the same of u) times NT rows, with the weights as the MMA's 128-row operand and the rows as its NT-column operand, so the
-// tensor cores' work follows the number of rows (16 at least) instead of 128-row tiles.
+// g and the same of u) times NT rows, with the weights as the MMA's 128-row operand and the rows
+// as its NT-column operand, so the tensor cores' work follows the number of rows (16 at least)
+// instead of 128-row tiles.
 //
 // Work is cut along the depth.  All tiles of all experts form one line of tiles x KB blocks
 // (a block: 64 deep in bf16, 128 in e4m3): an expert without rows has no tiles, and two busy
@@ -17,8 +18,8 @@
 // tile.  Nobody waits for another CTA.
 //
 // What bounds it: the bytes of the weights.  Stages of 32 KB of weights keep about 200 KB per
-// SM in flight (16 KB stages lost 10-15% to the hand-over of a stage).  Warp 0 loads (TMA), warp 1 issues MMAs and
-// owns TMEM, warps 2..5 take the accumulator out, warps 6..9 join parts: the memory fence, the
+// SM in flight (16 KB stages lost 10-15% to the hand-over of a stage).  Warp 0 loads (TMA), warp 1
+// issues MMAs and owns TMEM, warps 2..5 take the accumulator out, warps 6..9 join parts: the memory fence, the
 // arrival and the other parts' loads take several us beside a saturated memory, which the
 // accumulators of the next pieces must not wait for.  For 8-bit weights they do so after every
 // block, since its scales differ: acc += (xs ws) * block, as in fp8.cu.  `down` starts its
@@ -829,8 +830,8 @@ cudaError_t fp8_few(const Fp8Args& a) {
   return nt == 16 ? launch<kFp8, 16, kGluSilu>(tmW, tmX, f, a.num_sms, a.st) : launch<kFp8, 32, kGluSilu>(tmW, tmX, f, a.num_sms, a.st);
 }
 
-// When this file's kernels run (us, all experts full; here : 256 x 256 tiles).  The joining of
-// parts grows with the rows, so few rows win, and in bf16, where tiles come near the memory's
+// When this file's kernels run.  Measured with all experts full, in us, this file's kernels :
+// 256 x 256 tiles.  The joining of parts grows with the rows, so few rows win, and in bf16, where tiles come near the memory's
 // rate too, with 9 to 16 rows only many weights.
 //   gated experts, E x M x H, rows 1 / 8 / 16 / 32:
 //     1 x 1024 x 4096    19 : 24    22 : 23    27 : 23    37 : 23

@@ -241,7 +241,6 @@ __device__ __forceinline__ void load_gu(const CUtensorMap* tmGU, uint32_t tile, 
   tma_load_2d(tile + NARROW_BYTES, tmGU, bar, H + col, row0);
 }
 
-// MODE kUp, kUpSave, kDown, kDh, kDx.  tmD2: kUpSave the [g|u] output, kDh the [g|u] input.
 // The last, partial block of 64 rows of each expert of x and dy, zero-filled, to tx and tdy:
 // what the weight gradients read instead of the caller's rows past the last one.  Warp `gw` of
 // `warps` takes pieces of 128 x 16 bytes.
@@ -262,6 +261,7 @@ __device__ __forceinline__ void copy_tails(const PairArgs& a, const int* nrows, 
   }
 }
 
+// MODE kUp, kUpSave, kDown, kDh, kDx.  tmD2: kUpSave the [g|u] output, kDh the [g|u] input.
 template <int MODE, int FN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(MODE), 1)
     glu_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

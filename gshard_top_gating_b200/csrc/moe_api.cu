@@ -329,6 +329,8 @@ moe_status create_layer(moe_handle* out, int64_t S_max, int64_t M, int64_t H, in
 
 namespace {
 
+// The gated experts' products on the layer's own buffers (padded with zeros to a multiple of
+// 64 rows where the backward reduces over them, so without tail copies).
 GluArgs glu_args(moe_handle h, int64_t S, cudaStream_t st) {
   GluArgs a{};
   a.E = h->E;
@@ -512,8 +514,6 @@ struct NvtxStages {
   }
 };
 
-// The gated experts' products on the layer's own buffers (padded with zeros to a multiple of
-// 64 rows where the backward reduces over them, so without tail copies).
 moe_status forward_impl(moe_handle h, int64_t S, const void* x, void* y, cudaStream_t st) {
   if (!h || S < 0 || S > h->S_max) return MOE_ERR_INVALID_ARG;
   if (S > 0 && (!x || !y || !aligned(x, 16) || !aligned(y, 16))) return MOE_ERR_INVALID_ARG;

@@ -6,8 +6,10 @@
     g = ex.backward(x, counts, dy)                          # dx, dW13, dW2
 
 Expert e holds the first counts[e] of its C rows; the rows past them are neither read as
-data nor written.  The weights are borrowed by the C library; this object keeps
-references to them so they outlive the handle.
+data nor written.  Which kernels run goes by C, as the host does not see the counts: keep C
+close to the most rows that an expert holds.  The weights are borrowed by the C library; this
+object keeps references to them so they outlive the handle.  Its buffers serve all its calls,
+graphs captured from it included: one at a time, in the order of one stream.
 """
 from __future__ import annotations
 

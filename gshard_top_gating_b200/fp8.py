@@ -6,7 +6,8 @@
     y = mm(xq, xs, counts)                  # [E, C, N] bf16; counts int32 [E]
 
 A value stands for q * s of its block: 1 x 128 of a row, 128 x 128 of a weight matrix; a
-last block may be cut short.
+last block may be cut short.  As with GatedExperts, C chooses the kernels and an Fp8Matmul
+runs one call at a time.
 """
 from __future__ import annotations
 

@@ -93,7 +93,9 @@ class MoeLayer:
     def enable_backward(self) -> None:
         """Allocate the backward workspace now (moe_enable_backward).  Forwards
         that run after it also store the ReLU mask bits the backward reads; a
-        backward of a forward that ran before it re-reads h instead."""
+        backward of a forward that ran before it re-reads h instead.  Gated experts:
+        call it before the forward, which then keeps g and u; a backward of a
+        forward that ran before it is refused (MOE_ERR_STATE)."""
         if not getattr(self, "_bwd", False):
             L.moe_enable_backward(self.h)
             self._bwd = True
@@ -106,7 +108,9 @@ class MoeLayer:
         or the tensors of `out` (same keys) written in place.  With
         skip_empty_experts, dW1[e] and dW2[e] of experts that kept no token are
         left as they were (MOE_BWD_SKIP_EMPTY_EXPERTS).  The backward workspace is
-        allocated on the first call.
+        allocated on the first call (with gated experts too late for the forward
+        before it: see enable_backward).  Buffers of `out` hold at least what is
+        written, in its type.
         """
         self.enable_backward()
         for t in (x, dy):

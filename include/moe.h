@@ -18,6 +18,7 @@
  *             dropped (contributes zero, no renormalisation)
  *   xbuf[e, slot] = x[t]                               dispatch (on-device all-to-all)
  *   ybuf[e, :n_e] = relu(xbuf[e, :n_e] W1[e]) W2[e]    expert feed-forward networks
+ *                                                      (relu(v) = v > 0 ? v : 0, so 0 for a NaN)
  *   y[t]    = sum_{r kept} g_r ybuf[e_r, slot_r]        combine (second all-to-all)
  *   l_aux   = E * sum_j f_j P_j,  z = mean_t lse_t^2   auxiliary losses
  *
@@ -598,7 +599,12 @@ MOE_API const char* moe_backward_stage_name(int32_t stage);
  * Rows: x, y, dy and dx are [E, C, M] act, and nrows_dev [E] int32 (device) says how many
  * of its C rows each expert holds, read as min(max(nrows, 0), C).  Rows past that are not
  * read as data (they may hold anything, NaN included) and not written.  C may differ from
- * call to call, up to C_max.
+ * call to call, up to C_max.  The host does not see the counts, so which kernels run goes by
+ * C: for few rows (bf16: C up to 8, with many weights up to 16) the weights stream past the
+ * rows, else they are tiles of 256 rows.  A handful of rows in buffers of C = 1024 get the
+ * latter: give C close to the most rows that an expert holds.
+ *
+ * A handle's buffers serve all its calls, those captured into CUDA graphs too: one at a time.
  */
 typedef struct moe_glu* moe_glu_handle;
 
@@ -684,7 +690,8 @@ MOE_API moe_status moe_fp8_destroy(moe_fp8_handle h);
  * ceil(K/128)], for the rows each expert holds (nrows_dev [E] int32, device, read as
  * min(max(nrows, 0), C)); the other rows are not read as data and not written.
  *   y[m, n] = sum_kb xs[m, kb] ws[n / 128, kb] (sum_{k in kb} xq[m, k] wq[n, k])
- * with all sums in fp32 and one rounding to bf16.  0 <= C <= C_max; 16-byte aligned.
+ * with all sums in fp32 and one rounding to bf16.  0 <= C <= C_max; 16-byte aligned.  Up to
+ * C = 32 the weights stream past the rows, from 33 on tiles of 256 rows are multiplied.
  * Enqueued on `stream`, no host synchronisation.
  */
 MOE_API moe_status moe_fp8_matmul(moe_fp8_handle h, int64_t C, const void* xq_dev, const float* xs_dev,
